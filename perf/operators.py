@@ -222,11 +222,11 @@ def _inputs(case, seed):
 def _minmax(x, bits, dim):
     """Groupwise asymmetric codes of fp16 x: one rounding at a time in 32 bits."""
     mn, mx = x.amin(dim, keepdim=True).float(), x.amax(dim, keepdim=True).float()
-    top = float(2 ** bits - 1)
+    top = torch.full_like(mx, float(2 ** bits - 1))     # a tensor: by a number torch multiplies with 1 / top
     s = ((mx - mn) / top).half()
     s = torch.where(s == 0, torch.zeros_like(s), s)
     z = (mn + 0.0).half()
-    c = torch.round((x.float() - z.float()) / s.float()).clamp(0.0, top)
+    c = torch.round((x.float() - z.float()) / s.float()).clamp(0.0, float(2 ** bits - 1))
     c = torch.where(s == 0, torch.zeros_like(c), c)
     return c.to(torch.uint8), s, z
 
