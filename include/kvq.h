@@ -79,7 +79,9 @@
  * (each page is the (b, h) layout above restricted to one group), and block_table
  * int32 [B][Lcap/group_k] maps a sequence's group g to its page.  The library hands out
  * pages (prefill, and an append that quantizes a window group) and takes them back
- * (a new prefill of the sequence, kvq_release_sequence), and writes the table; the
+ * (a new prefill of the sequence, kvq_release_sequence), and writes the table.  A fork
+ * shares its parent's pages, which are never rewritten: a page is free again when no
+ * sequence holds it (kvq_fork_sequences, kvq_compact_pages).  The
  * window and retained buffers stay per sequence.  Needs quantized keys and values;
  * 1 <= n_pages, n_pages*Hkv*group_k < 2^30.
  *
@@ -127,7 +129,8 @@ extern "C" {
 
 #define KVQ_MAX_RETAINED      32
 
-/* Device status bits, written into the first word of a decode workspace. */
+/* Device status bits, written into the first word of a decode workspace (of a chunk
+ * attention: into the status word it is given). */
 #define KVQ_STATUS_TIMEOUT    1u  /* a bounded wait in the decode kernel gave up */
 
 typedef struct kvq_config {
@@ -238,6 +241,59 @@ int kvq_append_ragged(kvq_cache* cache, const void* k_new, const void* v_new,
 int kvq_prefill_sequence(kvq_cache* cache, int b, const void* k, const void* v, int L, void* stream);
 int kvq_release_sequence(kvq_cache* cache, int b);
 int kvq_free_pages(const kvq_cache* cache);
+
+/* Attention of several new tokens per sequence (drafted tokens to verify, a tree of drafts, a
+ * chunk of a prompt; no counterpart on the pages, whose decode step has one).  The new tokens
+ * are not in the cache and this call does not put them there (kvq_append_tokens does).
+ * q fp16 [B][Hq][T][d_k], k_new fp16 [B][Hkv][T][d_k], v_new fp16 [B][Hkv][T][d_v], T >= 1:
+ * sequence b's first counts[b] tokens are valid (counts: host int[B], each in [0, T]; NULL: T
+ * each); rows behind them are neither read nor, in out fp16 [B][Hq][T][d_v], written.  Token t
+ * of a sequence attends over all of the sequence's cached tokens and over the new tokens it
+ * sees: tokens 0 .. t, or, with mask (device u32 [B][T][ceil(T/32)]), the tokens j with bit
+ * j % 32 of word j / 32 of its row set, in any pattern (those behind counts[b] never).  A
+ * sequence may be empty; a row that sees nothing at all gives zeros.  Scores, side codes and
+ * rotation as for kvq_decode_attention, the new tokens counting as fp16 tokens.
+ * The tensor-core path rounds each decoded key and value and each softmax weight to fp16 once;
+ * sums, maxima and accumulators are fp32.
+ * workspace: device scratch of kvq_chunk_workspace_size bytes (0: may be NULL), for the cache's
+ * current lengths, T and num_splits (0 = automatic, else splits of the tokens of each row,
+ * clamped).  status: device u32 the kernel ORs KVQ_STATUS_* bits into, never cleared here; the
+ * first word of a decode workspace serves.  T * n_q_heads < 2^24 and B * T * n_q_heads < 2^31
+ * (UNSUPPORTED otherwise); counts or lengths that differ need B <= KVQ_MAX_SEQS.
+ * Runs on the device of the cache's buffers.  Errors: INVALID_ARG, UNSUPPORTED, ALIGN (mask
+ * and status: 4 bytes), WORKSPACE, CUDA. */
+int kvq_chunk_workspace_size(const kvq_cache* cache, int T, int num_splits, size_t* bytes);
+int kvq_chunk_attention(kvq_cache* cache, const void* q, const void* k_new, const void* v_new, int T,
+                        const int* counts, const void* mask, void* out, void* workspace,
+                        size_t workspace_bytes, int num_splits, void* status, void* stream);
+
+/* Append counts[b] tokens to each sequence (counts: host int[B], each in [0, T]; NULL: T each):
+ * the state, bit for bit, after that many kvq_append calls, in one or two launches.  k_new fp16
+ * [B][Hkv][T][d_k], v_new fp16 [B][Hkv][T][d_v]; token i of sequence b is row i of its chunk or,
+ * with index (device int32 [B][T]), row index[b][i], which may name any row any number of times
+ * (a value outside [0, T) reads row 0; entries behind counts[b] are not read).  Sequences with
+ * count 0 may be empty.  Errors: STATE (a sequence that takes tokens is empty), CAPACITY (past
+ * max_context; a page pool with too few free pages; nothing changes), UNSUPPORTED (lengths or
+ * counts that differ with B > KVQ_MAX_SEQS), INVALID_ARG, ALIGN (index: 4 bytes), CUDA. */
+int kvq_append_tokens(kvq_cache* cache, const void* k_new, const void* v_new, int T, const int* counts,
+                      const void* index, void* stream);
+
+/* Fork sequences: for each i < n, sequence dst[i] becomes a copy of src[i] (host int[n]) and goes
+ * its own way from there; what dst[i] held is released.  A parent may have several branches; a
+ * branch may appear once and must not be a parent of the same call (INVALID_ARG).  In a paged
+ * cache the branch shares its parent's pages and only its block-table row, window and retained
+ * tokens are copied; otherwise the quantized prefix is copied too.  n = 0 does nothing.
+ * Errors: INVALID_ARG, STATE (a parent is empty; nothing changes), CAPACITY (host memory), CUDA. */
+int kvq_fork_sequences(kvq_cache* cache, const int* src, const int* dst, int n, void* stream);
+
+/* Gather the pages in use at one end of a paged cache's pool, so that the rest of the pool's
+ * buffers can be given back or reused: the i-th lowest page outside that end moves to the i-th
+ * lowest free page inside it, and the block table follows.  Pages handed out later are those
+ * nearest the packed end.  Returns the number of pages in use (>= 0), or INVALID_ARG, UNSUPPORTED
+ * (the cache is not paged), CAPACITY (host memory), CUDA. */
+#define KVQ_COMPACT_LOW     0
+#define KVQ_COMPACT_HIGH    1
+int kvq_compact_pages(kvq_cache* cache, int end, void* stream);
 
 /* Reverse water-filling ("Attention-Aware Transform Coding (AATC)", §Méthodologie,
  * Allocation de Bits; host only): widths[i] in {0, 1, 2, 4, 8} for n units of weight

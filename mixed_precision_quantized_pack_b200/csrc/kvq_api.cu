@@ -12,6 +12,7 @@
 
 #include "../../include/kvq.h"
 #include "kvq_internal.cuh"
+#include "seq_ops.cuh"
 
 struct kvq_cache {
   kvq::Dims d;
@@ -21,6 +22,8 @@ struct kvq_cache {
   std::vector<int> table;   // paged: host copy of the block table [B][max_groups]
   std::vector<int> free_pages;   // paged: pages not in use, the next one handed out last
   std::vector<int> held;         // paged: pages of each sequence, its table entries [0, held)
+  std::vector<int> refs;         // paged: sequences that hold each page (forks share pages)
+  int device;                    // the device of the buffers
   int sm_count;
   int kernel;     // KVQ_KERNEL_*
   int centering;  // KVQ_CENTER_*
@@ -353,10 +356,19 @@ int pages_held(const kvq_cache* c, int b) { return c->d.paged ? c->held[b] : 0; 
 void release_pages(kvq_cache* c, int b) {
   const int mg = c->d.max_groups;
   for (int g = pages_held(c, b) - 1; g >= 0; --g) {
-    c->free_pages.push_back(c->table[b * mg + g]);
-    c->table[b * mg + g] = -1;
+    const int page = c->table[static_cast<size_t>(b) * mg + g];
+    if (--c->refs[page] == 0) c->free_pages.push_back(page);
+    c->table[static_cast<size_t>(b) * mg + g] = -1;
   }
   if (c->d.paged) c->held[b] = 0;
+}
+
+// Pages that releasing sequence b would free: those it shares with no other.
+int pages_freed_by(const kvq_cache* c, int b) {
+  int n = 0;
+  for (int g = 0; g < pages_held(c, b); ++g)
+    n += c->refs[c->table[static_cast<size_t>(b) * c->d.max_groups + g]] == 1;
+  return n;
 }
 
 // Collects block-table writes and launches them in batches of a launch parameter's size.
@@ -378,6 +390,7 @@ struct TableWriter {
     c->free_pages.pop_back();
     const int idx = b * c->d.max_groups + c->held[b]++;
     c->table[idx] = page;
+    c->refs[page] = 1;
     tw.idx[tw.n] = idx;
     tw.page[tw.n] = page;
     if (++tw.n == static_cast<int>(sizeof(tw.idx) / sizeof(tw.idx[0]))) flush();
@@ -489,6 +502,12 @@ int kvq_cache_init(const kvq_config* cfg, const kvq_buffers* bufs, kvq_cache** o
 #endif
   kvq_cache* c = new (std::nothrow) kvq_cache;
   if (!c) return KVQ_ERR_INVALID_ARG;
+  cudaPointerAttributes at;
+  c->device = dev;
+  if (cudaPointerGetAttributes(&at, bufs->win_k) == cudaSuccess && at.type == cudaMemoryTypeDevice)
+    c->device = at.device;
+  else
+    cudaGetLastError();
   c->d = d;
   c->d.sm_count = sms;
   c->buf = *bufs;
@@ -498,6 +517,7 @@ int kvq_cache_init(const kvq_config* cfg, const kvq_buffers* bufs, kvq_cache** o
   if (d.paged) {
     c->table.assign(static_cast<size_t>(d.B) * d.max_groups, -1);
     c->held.assign(d.B, 0);
+    c->refs.assign(cfg->n_pages, 0);
     // handed out from the back: a fresh pool gives pages 0, 1, 2, ... in order
     for (int p = cfg->n_pages - 1; p >= 0; --p) c->free_pages.push_back(p);
   }
@@ -651,12 +671,9 @@ int prefill_all(kvq_cache* c, const __half* kh, const __half* vh, int L_max, con
                 cudaStream_t s) {
   const kvq::Dims& d = c->d;
   if (d.paged) {
-    long long need = 0, avail = static_cast<long long>(c->free_pages.size());
-    for (int b = 0; b < d.B; ++b) {
-      need += quantized_prefix(d, lengths[b]) / d.gk;
-      avail += pages_held(c, b);
-    }
-    if (need > avail) return KVQ_ERR_CAPACITY;
+    long long need = 0;      // every page comes back first
+    for (int b = 0; b < d.B; ++b) need += quantized_prefix(d, lengths[b]) / d.gk;
+    if (need > d.n_pages) return KVQ_ERR_CAPACITY;
   }
   for (int b = 0; b < d.B; ++b) {
     release_pages(c, b);
@@ -725,7 +742,7 @@ int kvq_prefill_sequence(kvq_cache* c, int b, const void* k, const void* v, int 
   if (b < 0 || b >= d.B || L < 1 || L > d.max_context) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v)) return KVQ_ERR_ALIGN;
   const int Q = quantized_prefix(d, L);
-  if (d.paged && Q / d.gk > static_cast<int>(c->free_pages.size()) + pages_held(c, b))
+  if (d.paged && Q / d.gk > static_cast<int>(c->free_pages.size()) + pages_freed_by(c, b))
     return KVQ_ERR_CAPACITY;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   release_pages(c, b);
@@ -978,7 +995,11 @@ const char* kvq_debug_site_name(unsigned int site) {
       "retained: source", "retained: destination", "retained update: source",
       "block table: entry", "block table: page", "decode: block table entry",
       "decode: quantized group", "decode: key (scale, zero) group", "decode: retained slot",
-      "decode: window slot", "decode: partial row"};
+      "decode: window slot", "decode: partial row",
+      "append tokens: source", "append tokens: window slot", "append tokens: token row",
+      "append tokens: group", "fork: source", "fork: destination", "page move: source",
+      "page move: destination", "chunk: token row", "chunk: group", "chunk: block table entry",
+      "chunk: fp16 row", "chunk: partial row"};
   static_assert(sizeof(kNames) / sizeof(kNames[0]) == kvq::kSiteCount, "one name per site");
   return site < kvq::kSiteCount ? kNames[site] : "unknown";
 }
@@ -994,6 +1015,330 @@ int kvq_read_status(const void* workspace, unsigned int* status, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(s) != cudaSuccess) return KVQ_ERR_CUDA;
   return check_cuda(cudaMemcpy(status, workspace, sizeof(unsigned int), cudaMemcpyDeviceToHost));
+}
+
+}  // extern "C"
+
+// ---------------- several tokens per sequence, whole sequences ----------------
+namespace {
+
+// Makes the cache's device current for a call and puts the caller's back.
+struct DeviceScope {
+  int before = -1;
+  bool ok = true;
+  explicit DeviceScope(int device) {
+    ok = cudaGetDevice(&before) == cudaSuccess && (before == device || cudaSetDevice(device) == cudaSuccess);
+    if (!ok) cudaGetLastError();
+    if (before == device) before = -1;
+  }
+  ~DeviceScope() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+};
+
+// The body of an entry point; host memory that runs out is an error code, not an exception.
+template <typename F>
+int guarded(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return KVQ_ERR_CAPACITY;
+  }
+}
+
+kvq::CacheOut cache_out(const kvq_cache* c) {
+  kvq::CacheOut o;
+  o.kcode = static_cast<uint32_t*>(c->buf.kcode);
+  o.ksz = static_cast<__half2*>(c->buf.ksz);
+  o.vcode = static_cast<uint32_t*>(c->buf.vcode);
+  o.vsz = static_cast<__half2*>(c->buf.vsz);
+  o.win_k = static_cast<__half*>(c->buf.win_k);
+  o.win_v = static_cast<__half*>(c->buf.win_v);
+  o.ret_k = static_cast<__half*>(c->buf.ret_k);
+  o.ret_v = static_cast<__half*>(c->buf.ret_v);
+  o.zcode = static_cast<uint8_t*>(c->buf.zcode);
+  o.zsz = static_cast<__half2*>(c->buf.zsz);
+  o.side_u = static_cast<const float*>(c->buf.side_u);
+  o.table = static_cast<int*>(c->buf.block_table);
+  return o;
+}
+
+// Lengths and new-token counts of every sequence (counts null: T each) as a launch parameter.
+int seq_chunk(const kvq_cache* c, int T, const int* counts, kvq::SeqChunk* w) {
+  bool same = c->uniform();
+  for (int b = 1; b < c->d.B && counts; ++b) same = same && counts[b] == counts[0];
+  if (!same && c->d.B > kvq::kMaxSeqs) return KVQ_ERR_UNSUPPORTED;
+  w->uniform = same ? 1 : 0;
+  for (int b = 0; b < (same ? 1 : c->d.B); ++b) {
+    w->L[b] = c->L[b];
+    w->Q[b] = c->Q[b];
+    w->n[b] = counts ? counts[b] : T;
+  }
+  return KVQ_OK;
+}
+
+int check_counts(const kvq_cache* c, int T, const int* counts) {
+  if (T < 1) return KVQ_ERR_INVALID_ARG;
+  for (int b = 0; b < c->d.B && counts; ++b)
+    if (counts[b] < 0 || counts[b] > T) return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
+
+// How a chunk attention runs: its split count and its workspace.
+struct ChunkPlan {
+  int splits;
+  size_t ml, o, rot_q, rot_k, bytes;   // offsets of the workspace's parts, and its size
+};
+
+int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
+  const kvq::Dims& d = c->d;
+  if (T < 1 || num_splits < 0) return KVQ_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(d.B) * d.Hq * T;
+  if (rows >= (1LL << 31) || static_cast<long long>(d.Hq) * T >= (1LL << 24)) return KVQ_ERR_UNSUPPORTED;
+  int longest = 0;
+  for (int b = 0; b < d.B; ++b) longest = std::max(longest, c->L[b]);
+  p->splits = kvq::chunk_splits(d, longest, T, num_splits);
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up(bytes);
+    return here;
+  };
+  const bool partials = p->splits > 1;
+  p->ml = take(partials ? rows * p->splits * sizeof(float2) : 0);
+  p->o = take(partials ? rows * p->splits * d.dv * sizeof(float) : 0);
+  p->rot_q = take(d.rot ? rows * d.dk * 2 : 0);
+  p->rot_k = take(d.rot ? static_cast<size_t>(d.B) * d.Hkv * T * d.dk * 2 : 0);
+  p->bytes = at;
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kvq_chunk_workspace_size(const kvq_cache* c, int T, int num_splits, size_t* bytes) {
+  if (!c || !bytes) return KVQ_ERR_INVALID_ARG;
+  ChunkPlan p;
+  const int rc = plan_chunk(c, T, num_splits, &p);
+  if (rc) return rc;
+  *bytes = p.bytes;
+  return KVQ_OK;
+}
+
+int kvq_chunk_attention(kvq_cache* c, const void* q, const void* k_new, const void* v_new, int T,
+                        const int* counts, const void* mask, void* out, void* workspace,
+                        size_t workspace_bytes, int num_splits, void* status, void* stream) {
+  if (!c || !q || !k_new || !v_new || !out || !status) return KVQ_ERR_INVALID_ARG;
+  int rc = check_counts(c, T, counts);
+  if (rc) return rc;
+  const kvq::Dims& d = c->d;
+  ChunkPlan p;
+  rc = plan_chunk(c, T, num_splits, &p);
+  if (rc) return rc;
+  if (p.bytes && !workspace) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) || !aligned16(workspace))
+    return KVQ_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(mask) | reinterpret_cast<uintptr_t>(status)) & 3u) return KVQ_ERR_ALIGN;
+  if (workspace_bytes < p.bytes) return KVQ_ERR_WORKSPACE;
+  kvq::ChunkArgs a;
+  rc = seq_chunk(c, T, counts, &a.seq);
+  if (rc) return rc;
+  DeviceScope on(c->device);
+  if (!on.ok) return KVQ_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  a.T = T;
+  a.splits = p.splits;
+  a.score_scale = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(d.dk)));
+  a.q = static_cast<const __half*>(q);
+  a.k_new = static_cast<const __half*>(k_new);
+  a.v_new = static_cast<const __half*>(v_new);
+  a.mask = static_cast<const uint32_t*>(mask);
+  a.out = static_cast<__half*>(out);
+  a.ml = reinterpret_cast<float2*>(ws + p.ml);
+  a.o = reinterpret_cast<float*>(ws + p.o);
+  a.status = static_cast<unsigned int*>(status);
+  if (d.rot) {
+    __half* rq = reinterpret_cast<__half*>(ws + p.rot_q);
+    __half* rk = reinterpret_cast<__half*>(ws + p.rot_k);
+    rc = check_cuda(kvq::launch_rotate_rows(d, a.q, rq, static_cast<long long>(d.B) * d.Hq * T, d.rot_inv_cq, s));
+    if (!rc)
+      rc = check_cuda(kvq::launch_rotate_rows(d, a.k_new, rk, static_cast<long long>(d.B) * d.Hkv * T, d.rot_inv_ck, s));
+    if (rc) return rc;
+    a.q = rq;
+    a.k_new = rk;
+  }
+  const kvq::CacheBufs cb = cache_bufs(c);
+  rc = check_cuda(kvq::launch_chunk_simple(d, cb, a, s));
+  if (!rc && a.splits > 1) rc = check_cuda(kvq::launch_chunk_combine(d, a, s));
+  return rc;
+}
+
+int kvq_append_tokens(kvq_cache* c, const void* k_new, const void* v_new, int T, const int* counts,
+                      const void* index, void* stream) {
+  if (!c || !k_new || !v_new) return KVQ_ERR_INVALID_ARG;
+  int rc = check_counts(c, T, counts);
+  if (rc) return rc;
+  const kvq::Dims& d = c->d;
+  int max_groups = 0, max_tail = 0;
+  long long pages = 0;
+  for (int b = 0; b < d.B; ++b) {
+    const int n = counts ? counts[b] : T;
+    if (n == 0) continue;
+    if (c->L[b] < 1) return KVQ_ERR_STATE;
+    if (n > d.max_context - c->L[b]) return KVQ_ERR_CAPACITY;
+    const int Q2 = quantized_prefix(d, c->L[b] + n);
+    const int g = (Q2 - c->Q[b]) / d.gk;
+    max_groups = std::max(max_groups, g);
+    max_tail = std::max(max_tail, c->L[b] + n - std::max(c->L[b], Q2));
+    pages += g;
+  }
+  if (d.paged && pages > static_cast<long long>(c->free_pages.size())) return KVQ_ERR_CAPACITY;
+  if (!aligned16(k_new) || !aligned16(v_new)) return KVQ_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(index) & 3u) return KVQ_ERR_ALIGN;
+  kvq::SeqChunk w;
+  rc = seq_chunk(c, T, counts, &w);
+  if (rc) return rc;
+  DeviceScope on(c->device);
+  if (!on.ok) return KVQ_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d.paged && pages) {
+    TableWriter tw(c, s);
+    for (int b = 0; b < d.B; ++b) {
+      const int n = counts ? counts[b] : T;
+      for (int g = (quantized_prefix(d, c->L[b] + n) - c->Q[b]) / d.gk; n && g > 0; --g) tw.assign(b);
+    }
+    if (tw.flush()) return tw.rc;
+  }
+  rc = check_cuda(kvq::launch_append_tokens(d, cache_out(c), w, static_cast<const __half*>(k_new),
+                                            static_cast<const __half*>(v_new), T,
+                                            static_cast<const int*>(index), max_groups, max_tail, s));
+  if (rc) return rc;
+  for (int b = 0; b < d.B; ++b) {
+    const int n = counts ? counts[b] : T;
+    if (n == 0) continue;
+    c->L[b] += n;
+    c->Q[b] = quantized_prefix(d, c->L[b]);
+  }
+  return KVQ_OK;
+}
+
+int kvq_fork_sequences(kvq_cache* c, const int* src, const int* dst, int n, void* stream) {
+  if (!c || n < 0 || (n > 0 && (!src || !dst))) return KVQ_ERR_INVALID_ARG;
+  if (n == 0) return KVQ_OK;
+  return guarded([&]() -> int {
+    const kvq::Dims& d = c->d;
+    std::vector<char> role(d.B, 0);      // 1: a parent, 2: a branch
+    for (int i = 0; i < n; ++i) {
+      if (src[i] < 0 || src[i] >= d.B || dst[i] < 0 || dst[i] >= d.B) return KVQ_ERR_INVALID_ARG;
+      role[src[i]] = 1;
+    }
+    for (int i = 0; i < n; ++i) {
+      if (role[dst[i]] != 0) return KVQ_ERR_INVALID_ARG;
+      role[dst[i]] = 2;
+    }
+    for (int i = 0; i < n; ++i)
+      if (c->L[src[i]] < 1) return KVQ_ERR_STATE;
+    DeviceScope on(c->device);
+    if (!on.ok) return KVQ_ERR_CUDA;
+    const int mg = d.max_groups;
+    if (d.paged) {
+      // room for every page that may be freed, so that nothing below can throw half way
+      c->free_pages.reserve(d.n_pages);
+      for (int i = 0; i < n; ++i) release_pages(c, dst[i]);
+      for (int i = 0; i < n; ++i) {
+        for (int g = 0; g < c->held[src[i]]; ++g) {
+          const int page = c->table[static_cast<size_t>(src[i]) * mg + g];
+          c->table[static_cast<size_t>(dst[i]) * mg + g] = page;
+          ++c->refs[page];
+        }
+        c->held[dst[i]] = c->held[src[i]];
+      }
+    }
+    for (int i0 = 0; i0 < n; i0 += kvq::kMaxSeqs) {
+      kvq::ForkList f;
+      f.n = std::min(n - i0, kvq::kMaxSeqs);
+      for (int i = 0; i < f.n; ++i) {
+        f.src[i] = src[i0 + i];
+        f.dst[i] = dst[i0 + i];
+        f.L[i] = c->L[f.src[i]];
+        f.Q[i] = c->Q[f.src[i]];
+      }
+      const int rc = check_cuda(kvq::launch_fork(d, cache_out(c), f, static_cast<cudaStream_t>(stream)));
+      if (rc) return rc;
+    }
+    for (int i = 0; i < n; ++i) {
+      c->L[dst[i]] = c->L[src[i]];
+      c->Q[dst[i]] = c->Q[src[i]];
+    }
+    return KVQ_OK;
+  });
+}
+
+int kvq_compact_pages(kvq_cache* c, int end, void* stream) {
+  if (!c || (end != KVQ_COMPACT_LOW && end != KVQ_COMPACT_HIGH)) return KVQ_ERR_INVALID_ARG;
+  if (!c->d.paged) return KVQ_ERR_UNSUPPORTED;
+  return guarded([&]() -> int {
+    const kvq::Dims& d = c->d;
+    const int used = d.n_pages - static_cast<int>(c->free_pages.size());
+    const int lo = end == KVQ_COMPACT_HIGH ? d.n_pages - used : 0, hi = lo + used;
+    // the i-th lowest used page outside [lo, hi) goes to the i-th lowest free page inside it
+    std::vector<int> from, to(d.n_pages, -1);
+    for (int p = 0; p < d.n_pages; ++p)
+      if (c->refs[p] > 0 && (p < lo || p >= hi)) from.push_back(p);
+    std::vector<kvq::PageMoves> batch(1);
+    kvq::PageMoves& m = batch[0];
+    DeviceScope on(c->device);
+    if (!on.ok) return KVQ_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    m.n_moves = m.n_writes = 0;
+    auto flush = [&]() -> int {
+      const int rc = check_cuda(kvq::launch_page_moves(d, cache_out(c), m, s));
+      m.n_moves = m.n_writes = 0;
+      return rc;
+    };
+    size_t next = 0;
+    for (int p = lo; p < hi; ++p) {
+      if (c->refs[p] > 0) continue;
+      m.src[m.n_moves] = from[next];
+      m.dst[m.n_moves] = p;
+      to[from[next++]] = p;
+      if (++m.n_moves == kvq::PageMoves::kCap) {
+        const int rc = flush();
+        if (rc) return rc;
+      }
+    }
+    for (int b = 0; b < d.B; ++b)
+      for (int g = 0; g < c->held[b]; ++g) {
+        const size_t idx = static_cast<size_t>(b) * d.max_groups + g;
+        if (to[c->table[idx]] < 0) continue;
+        m.idx[m.n_writes] = static_cast<int>(idx);
+        m.page[m.n_writes] = to[c->table[idx]];
+        if (++m.n_writes == kvq::PageMoves::kCap) {
+          const int rc = flush();
+          if (rc) return rc;
+        }
+      }
+    const int rc = flush();
+    if (rc) return rc;
+    // host state: references and tables move along; the next page handed out is the free one
+    // nearest the packed end
+    for (int p : from) {
+      c->refs[to[p]] = c->refs[p];
+      c->refs[p] = 0;
+    }
+    for (int b = 0; b < d.B; ++b)
+      for (int g = 0; g < c->held[b]; ++g) {
+        int& page = c->table[static_cast<size_t>(b) * d.max_groups + g];
+        if (to[page] >= 0) page = to[page];
+      }
+    const size_t n_free = c->free_pages.size();
+    for (size_t i = 0; i < n_free; ++i)
+      c->free_pages[i] = end == KVQ_COMPACT_HIGH ? static_cast<int>(i) : d.n_pages - 1 - static_cast<int>(i);
+    return used;
+  });
 }
 
 }  // extern "C"

@@ -30,6 +30,9 @@ enum DebugSite : unsigned int {
   kSiteRetSrc, kSiteRetDst, kSiteRetUpd,
   kSiteTableIdx, kSiteTablePage,
   kSiteDecTable, kSiteDecKCode, kSiteDecKMeta, kSiteDecRetK, kSiteDecWinK, kSiteDecPartial,
+  kSiteTokSrc, kSiteTokWin, kSiteTokRow, kSiteTokGroup,       // multi-token append
+  kSiteForkSrc, kSiteForkDst, kSitePageSrc, kSitePageDst,     // forks and page moves
+  kSiteChunkRow, kSiteChunkGroup, kSiteChunkTable, kSiteChunkFp16, kSiteChunkPartial,   // chunk attention
   kSiteCount
 };
 constexpr int kMaxSeqs = 256;   // sequences of a cache whose lengths may differ (per-launch arrays)

@@ -1,0 +1,108 @@
+// Internal declarations of the operators on several tokens per sequence and on whole
+// sequences: chunk attention, multi-token append, forks and page moves.
+#pragma once
+
+#include "kvq_internal.cuh"
+
+namespace kvq {
+
+// Lengths and new tokens of the sequences of one call (a launch parameter): sequence b holds
+// L[b] tokens, Q[b] of them quantized, and brings n[b] new ones (one entry for all sequences
+// when `uniform`).
+struct SeqChunk {
+  int uniform;
+  int L[kMaxSeqs], Q[kMaxSeqs], n[kMaxSeqs];
+};
+struct SeqNew {
+  int L, Q, n, n_ret;
+};
+__device__ __forceinline__ SeqNew seq_new(const SeqChunk& w, int b, int log_retain) {
+  const int i = w.uniform ? 0 : b;
+  SeqNew s;
+  s.L = w.L[i];
+  s.Q = w.Q[i];
+  s.n = w.n[i];
+  s.n_ret = log_retain ? retained_count(s.Q) : 0;
+  return s;
+}
+
+// Quantized prefix of a sequence of L tokens.
+__host__ __device__ inline int prefix_of(const Dims& d, int L) {
+  if (d.kb == 16) return 0;
+  const int over = L - d.R;
+  return over > 0 ? over / d.gk * d.gk : 0;
+}
+
+// Whether position p < Q is one of the retained tokens of a quantized prefix of Q tokens.
+__device__ __forceinline__ bool is_retained(int Q, int p) {
+  return (p & ((1 << (31 - __clz(Q - p))) - 1)) == 0;
+}
+
+// Device views of the cache buffers for the operators that write them.
+struct CacheOut {
+  uint32_t* kcode;
+  __half2* ksz;
+  uint32_t* vcode;
+  __half2* vsz;
+  __half* win_k;
+  __half* win_v;
+  __half* ret_k;
+  __half* ret_v;
+  uint8_t* zcode;
+  __half2* zsz;
+  const float* side_u;
+  int* table;
+};
+
+// ---- multi-token append (append_tokens.cu) ----
+// index: device int32 [B][T], the row of k / v that token i of a sequence is (null: row i).
+// max_groups_out / max_tail: the most groups any sequence quantizes, the most rows it keeps.
+cudaError_t launch_append_tokens(const Dims& d, const CacheOut& c, const SeqChunk& w, const __half* k,
+                                 const __half* v, int T, const int* index, int max_new_groups, int max_tail,
+                                 cudaStream_t s);
+
+// ---- forks and page moves (pages.cu) ----
+struct ForkList {
+  int n;
+  int src[kMaxSeqs], dst[kMaxSeqs], L[kMaxSeqs], Q[kMaxSeqs];
+};
+cudaError_t launch_fork(const Dims& d, const CacheOut& c, const ForkList& f, cudaStream_t s);
+
+// One batch of a compaction: pages to copy, and block-table entries to write.
+struct PageMoves {
+  static constexpr int kCap = 1984;   // four lists within the 32 KB of launch parameters
+  int n_moves, n_writes;
+  int src[kCap], dst[kCap];
+  int idx[kCap], page[kCap];
+};
+cudaError_t launch_page_moves(const Dims& d, const CacheOut& c, const PageMoves& m, cudaStream_t s);
+
+// ---- chunk attention ----
+// T query rows per head; a kv head's block of queries is n_rep * T contiguous rows, row
+// r = rep * T + t.  Splits of a (b, kv head, row block) write (m, l) and unnormalised outputs
+// per row to the workspace; one split writes `out` itself.
+struct ChunkArgs {
+  SeqChunk seq;
+  int T;                  // query rows per head, and rows per head of k_new / v_new
+  int splits;
+  float score_scale;      // log2(e) / sqrt(d_k)
+  const __half* q;        // [B][Hq][T][dk], rotated when the keys are
+  const __half* k_new;    // [B][Hkv][T][dk], likewise
+  const __half* v_new;    // [B][Hkv][T][dv]
+  const uint32_t* mask;   // [B][T][ceil(T / 32)], bit j of row t: t sees new token j; null: causal
+  __half* out;            // [B][Hq][T][dv]
+  float2* ml;             // [B * Hq * T][splits]
+  float* o;               // [B * Hq * T][splits][dv]
+  unsigned int* status;
+};
+
+// Splits of each (b, kv head, row block) for sequences of at most L cached tokens (num_splits > 0: that
+// many, clamped to the tokens).
+int chunk_splits(const Dims& d, int L, int T, int num_splits);
+cudaError_t launch_chunk_simple(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s);
+cudaError_t launch_chunk_combine(const Dims& d, const ChunkArgs& a, cudaStream_t s);
+// dst rows = rotations of src rows (rows of dk), scaled by inv_c
+cudaError_t launch_rotate_rows(const Dims& d, const __half* src, __half* dst, long long rows, float inv_c,
+                               cudaStream_t s);
+
+}  // namespace kvq

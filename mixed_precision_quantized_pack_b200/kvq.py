@@ -35,6 +35,8 @@ KVQ_CENTER_AUTO = 0
 KVQ_CENTER_OFF = 1
 KVQ_CENTER_ON = 2
 KVQ_STATUS_TIMEOUT = 1
+KVQ_COMPACT_LOW = 0
+KVQ_COMPACT_HIGH = 1
 KVQ_NOALLOC_SCRATCH_BYTES = 8 << 20
 KVQ_MAX_SEQS = 256
 
@@ -118,6 +120,11 @@ _SIGNATURES = {
     "kvq_prefill_sequence": (_I, [_P, _I, _P, _P, _I, _P]),
     "kvq_release_sequence": (_I, [_P, _I]),
     "kvq_free_pages": (_I, [_P]),
+    "kvq_chunk_workspace_size": (_I, [_P, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "kvq_chunk_attention": (_I, [_P, _P, _P, _P, _I, ctypes.POINTER(_I), _P, _P, _P, ctypes.c_size_t, _I, _P, _P]),
+    "kvq_append_tokens": (_I, [_P, _P, _P, _I, ctypes.POINTER(_I), _P, _P]),
+    "kvq_fork_sequences": (_I, [_P, ctypes.POINTER(_I), ctypes.POINTER(_I), _I, _P]),
+    "kvq_compact_pages": (_I, [_P, _I, _P]),
     "kvq_allocate_bits": (_I, [ctypes.POINTER(ctypes.c_double), _I, _I, _I, ctypes.POINTER(ctypes.c_ubyte)]),
 }
 
@@ -240,6 +247,38 @@ def kvq_free_pages(handle: int) -> int:
     return _check(lib().kvq_free_pages(handle), "kvq_free_pages")
 
 
+def _ints(values):
+    return None if values is None else (_I * len(values))(*[int(x) for x in values])
+
+
+def kvq_chunk_workspace_size(handle: int, T: int, num_splits: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().kvq_chunk_workspace_size(handle, int(T), int(num_splits), ctypes.byref(n)),
+           "kvq_chunk_workspace_size")
+    return int(n.value)
+
+
+def kvq_chunk_attention(handle: int, q_ptr: int, k_ptr: int, v_ptr: int, T: int, counts, mask_ptr: int,
+                        out_ptr: int, ws_ptr: int, ws_bytes: int, num_splits: int, status_ptr: int,
+                        stream: int) -> None:
+    _check(lib().kvq_chunk_attention(handle, q_ptr, k_ptr, v_ptr, int(T), _ints(counts), mask_ptr, out_ptr, ws_ptr,
+                                     int(ws_bytes), int(num_splits), status_ptr, stream), "kvq_chunk_attention")
+
+
+def kvq_append_tokens(handle: int, k_ptr: int, v_ptr: int, T: int, counts, index_ptr: int, stream: int) -> None:
+    _check(lib().kvq_append_tokens(handle, k_ptr, v_ptr, int(T), _ints(counts), index_ptr, stream),
+           "kvq_append_tokens")
+
+
+def kvq_fork_sequences(handle: int, src, dst, stream: int) -> None:
+    _check(lib().kvq_fork_sequences(handle, _ints(src), _ints(dst), len(src), stream), "kvq_fork_sequences")
+
+
+def kvq_compact_pages(handle: int, end: int, stream: int) -> int:
+    """The number of pages in use, now gathered at `end`."""
+    return _check(lib().kvq_compact_pages(handle, int(end), stream), "kvq_compact_pages")
+
+
 def kvq_get_seq_state(handle: int, b: int) -> Tuple[int, int, List[int]]:
     L, Q, n = _I(), _I(), _I()
     idx = (ctypes.c_int * KVQ_MAX_RETAINED)()
@@ -336,6 +375,13 @@ def _fp16_cuda(t: torch.Tensor, shape, name: str) -> torch.Tensor:
     return t
 
 
+def _int32_cuda(t: torch.Tensor, shape, device, name: str) -> torch.Tensor:
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: need a contiguous int32 tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
 class KVCache:
     """One attention layer's packed KV cache in device memory owned by PyTorch.
 
@@ -421,6 +467,84 @@ class KVCache:
 
     def free_pages(self) -> int:
         return kvq_free_pages(self.handle)
+
+    # several tokens per sequence, whole sequences: these run on the cache's own device
+    def _on_device(self, stream):
+        return _stream(torch.cuda.current_stream(self.view("win_k").device) if stream is None else stream)
+
+    def _new_tokens(self, k_new: torch.Tensor, v_new: torch.Tensor, counts):
+        c = self.cfg
+        if k_new.dim() != 4:
+            raise ValueError("k_new: need [batch][n_kv_heads][T][d_k]")
+        T, dev = k_new.shape[2], self.view("win_k").device
+        _fp16_cuda(k_new, (c["batch"], c["n_kv_heads"], T, c["d_k"]), "k_new")
+        _fp16_cuda(v_new, (c["batch"], c["n_kv_heads"], T, c["d_v"]), "v_new")
+        if k_new.device != dev or v_new.device != dev:
+            raise ValueError(f"k_new, v_new: need tensors on the cache's device {dev}")
+        if counts is not None:
+            counts = [int(x) for x in counts]
+            if len(counts) != c["batch"]:
+                raise ValueError("counts: one per sequence")
+        return T, dev, counts
+
+    def chunk_attention(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, counts=None,
+                        mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        num_splits: int = 0, stream=None) -> torch.Tensor:
+        """Attention of T new tokens per sequence over the cache and over each other.
+
+        q fp16 [B][Hq][T][d_k], k_new fp16 [B][Hkv][T][d_k], v_new fp16 [B][Hkv][T][d_v] ->
+        out fp16 [B][Hq][T][d_v].  Sequence b has counts[b] <= T tokens (None: T each); rows
+        behind them are left as they were (zeros when `out` is made here).  Causal among the
+        new tokens, or as `mask` says: int32 [B][T][ceil(T/32)], bit j of row t set where t sees
+        j.  The cache is unchanged: append_tokens takes the tokens that stay."""
+        c = self.cfg
+        T, dev, counts = self._new_tokens(k_new, v_new, counts)
+        _fp16_cuda(q, (c["batch"], c["n_q_heads"], T, c["d_k"]), "q")
+        if mask is not None:
+            _int32_cuda(mask, (c["batch"], T, -(-T // 32)), dev, "mask")
+        shape = (c["batch"], c["n_q_heads"], T, c["d_v"])
+        # what is allocated here belongs to the stream that the kernels run on
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        s = s if hasattr(s, "cuda_stream") else torch.cuda.ExternalStream(int(s), device=dev)
+        with torch.cuda.stream(s):
+            if out is None:
+                partly = counts is not None and min(counts) < T
+                out = (torch.zeros if partly else torch.empty)(shape, dtype=torch.float16, device=dev)
+            _fp16_cuda(out, shape, "out")
+            if q.device != dev or out.device != dev:
+                raise ValueError(f"q, out: need tensors on the cache's device {dev}")
+            n = kvq_chunk_workspace_size(self.handle, T, num_splits)
+            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        kvq_chunk_attention(self.handle, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), T, counts,
+                            mask.data_ptr() if mask is not None else None, out.data_ptr(),
+                            ws.data_ptr() if n else None, n, num_splits, self.workspace.data_ptr(), _stream(s))
+        return out
+
+    def append_tokens(self, k_new: torch.Tensor, v_new: torch.Tensor, counts=None,
+                      index: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Appends counts[b] (None: T) of the T new tokens to each sequence: the first ones, or
+        the rows that `index` (int32 [B][T]) names, in its order."""
+        T, dev, counts = self._new_tokens(k_new, v_new, counts)
+        if index is not None:
+            _int32_cuda(index, (self.cfg["batch"], T), dev, "index")
+        kvq_append_tokens(self.handle, k_new.data_ptr(), v_new.data_ptr(), T, counts,
+                          index.data_ptr() if index is not None else None, self._on_device(stream))
+
+    def fork(self, src, dst, stream=None) -> None:
+        """Sequence dst[i] becomes a branch of src[i] (ints, or lists of equal length)."""
+        src = [src] if isinstance(src, int) else list(src)
+        dst = [dst] if isinstance(dst, int) else list(dst)
+        if len(src) != len(dst):
+            raise ValueError("fork: one dst per src")
+        kvq_fork_sequences(self.handle, src, dst, self._on_device(stream))
+
+    def compact(self, end: str = "low", stream=None) -> int:
+        """Gathers a paged cache's pages in use at the "low" or "high" end of the pool; returns
+        how many there are."""
+        if end not in ("low", "high"):
+            raise ValueError('compact: end is "low" or "high"')
+        return kvq_compact_pages(self.handle, KVQ_COMPACT_HIGH if end == "high" else KVQ_COMPACT_LOW,
+                                 self._on_device(stream))
 
     def seq_state(self, b: int) -> Tuple[int, int, List[int]]:
         return kvq_get_seq_state(self.handle, b)
