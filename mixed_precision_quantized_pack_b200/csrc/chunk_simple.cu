@@ -294,7 +294,7 @@ rotate_rows_kernel(Dims d, const __half* __restrict__ src, __half* __restrict__ 
 
 }  // namespace
 
-int chunk_splits(const Dims& d, int L, int T, int num_splits) {
+int chunk_simple_splits(const Dims& d, int L, int T, int num_splits) {
   const int most = std::min(64, std::max(1, (L + T) / 64));       // at least 64 tokens a split
   if (num_splits > 0) return std::min(num_splits, most);
   const long long ctas = static_cast<long long>(d.B) * d.Hkv * ((d.n_rep * T + kRows - 1) / kRows);

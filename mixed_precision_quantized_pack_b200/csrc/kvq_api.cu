@@ -1086,6 +1086,7 @@ int check_counts(const kvq_cache* c, int T, const int* counts) {
 
 // How a chunk attention runs: its split count and its workspace.
 struct ChunkPlan {
+  bool tensor;                          // the tensor-core kernel
   int splits;
   size_t ml, o, rot_q, rot_k, bytes;   // offsets of the workspace's parts, and its size
 };
@@ -1097,7 +1098,8 @@ int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
   if (rows >= (1LL << 31) || static_cast<long long>(d.Hq) * T >= (1LL << 24)) return KVQ_ERR_UNSUPPORTED;
   int longest = 0;
   for (int b = 0; b < d.B; ++b) longest = std::max(longest, c->L[b]);
-  p->splits = kvq::chunk_splits(d, longest, T, num_splits);
+  p->tensor = c->kernel != KVQ_KERNEL_GENERIC && kvq::chunk_mma_supported(d);
+  p->splits = (p->tensor ? kvq::chunk_mma_splits : kvq::chunk_simple_splits)(d, longest, T, num_splits);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1171,7 +1173,7 @@ int kvq_chunk_attention(kvq_cache* c, const void* q, const void* k_new, const vo
     a.k_new = rk;
   }
   const kvq::CacheBufs cb = cache_bufs(c);
-  rc = check_cuda(kvq::launch_chunk_simple(d, cb, a, s));
+  rc = check_cuda((p.tensor ? kvq::launch_chunk_mma : kvq::launch_chunk_simple)(d, cb, a, s));
   if (!rc && a.splits > 1) rc = check_cuda(kvq::launch_chunk_combine(d, a, s));
   return rc;
 }

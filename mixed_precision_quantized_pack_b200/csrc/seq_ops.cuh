@@ -97,8 +97,11 @@ struct ChunkArgs {
 };
 
 // Splits of each (b, kv head, row block) for sequences of at most L cached tokens (num_splits > 0: that
-// many, clamped to the tokens).
-int chunk_splits(const Dims& d, int L, int T, int num_splits);
+// many, clamped to the tokens), for either kernel.
+int chunk_simple_splits(const Dims& d, int L, int T, int num_splits);
+int chunk_mma_splits(const Dims& d, int L, int T, int num_splits);
+bool chunk_mma_supported(const Dims& d);
+cudaError_t launch_chunk_mma(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s);
 cudaError_t launch_chunk_simple(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s);
 cudaError_t launch_chunk_combine(const Dims& d, const ChunkArgs& a, cudaStream_t s);
 // dst rows = rotations of src rows (rows of dk), scaled by inv_c
