@@ -17,7 +17,7 @@
 // fp16 once.  Tokens behind the end of the prefix in its last tile repeat the last row: their
 // weights are 0 and their values finite.
 //
-// NT, here and below, is the number of producer threads (256 or 512).
+// NT, here and below, is the number of threads that share a tile's keys or values (256).
 #pragma once
 
 #include <algorithm>
@@ -535,17 +535,18 @@ __device__ __forceinline__ void clear_ring(const Dims& d, uint32_t ring, int sta
   ptx::fence_proxy_async_smem();
 }
 
-template <int NT, int EMPTY>
-__device__ __forceinline__ void init_token_bars(uint32_t bars) {
+// Arrivals a phase: `producers` warps that write keys, as many that write values, `readers` warps of
+// the packed ring, `users` MMA streams of a tile.
+__device__ __forceinline__ void init_token_bars(uint32_t bars, int producers, int readers, int users) {
   for (int i = 0; i < 2; ++i) {
-    ptx::mbar_init(bars + 8 * (kKFull + i), NT / 32);
-    ptx::mbar_init(bars + 8 * (kKEmpty + i), EMPTY);
-    ptx::mbar_init(bars + 8 * (kVFull + i), NT / 32);
-    ptx::mbar_init(bars + 8 * (kVEmpty + i), EMPTY);
+    ptx::mbar_init(bars + 8 * (kKFull + i), producers);
+    ptx::mbar_init(bars + 8 * (kKEmpty + i), users);
+    ptx::mbar_init(bars + 8 * (kVFull + i), producers);
+    ptx::mbar_init(bars + 8 * (kVEmpty + i), users);
   }
   for (int i = 0; i < kMaxRing; ++i) {
     ptx::mbar_init(bars + 8 * (kRingFull + i), 1);
-    ptx::mbar_init(bars + 8 * (kRingEmpty + i), NT / 32);
+    ptx::mbar_init(bars + 8 * (kRingEmpty + i), readers);
   }
 }
 
@@ -638,9 +639,11 @@ __device__ __forceinline__ void copy_tiles(const Ctx& c, const Tiles& t, int lan
   copier.drain(c, lane, bars, false);
 }
 
-// The producers' loop: tiles t.begin .. t.end of the CTA into stages 0, 1, 0, ... of K and V.  SELF:
-// their first warp copies the packed tiles as well.
-template <int KB, int VB, int DK, int NT, bool SELF>
+// The loop of NT producer threads: tiles t.begin .. t.end of the CTA into stages 0, 1, 0, ... of K and
+// V.  PART: both, or the keys or the values alone (two groups of producers, whose waits then
+// overlap with the other's decoding).  SELF: the first warp copies the packed tiles as well.
+enum Part { kBoth, kKeys, kValues };
+template <int KB, int VB, int DK, int NT, Part PART, bool SELF>
 __device__ __forceinline__ void produce(const Ctx& c, const Tiles& t, int tid, uint32_t kdst0, uint32_t vdst0,
                                         uint32_t bars, const Waiter& wait) {
   constexpr int kKeyStage = (DK > 64 ? DK / 64 : 1) * kHalf;
@@ -649,54 +652,57 @@ __device__ __forceinline__ void produce(const Ctx& c, const Tiles& t, int tid, u
   const int lane = tid & 31;
   const int n = t.end - t.begin;
   const int packed = kPacked ? max(0, min(t.end, t.nq) - t.begin) : 0;      // the CTA's first tiles
-  bool live = true;
-  Copier<KB, VB, DK> copier;
-  if constexpr (kPacked && SELF)
-    if (tid < 32) copier.start(c, t, packed, lane, bars);
   auto arrive = [&](int bar) {
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * bar);
   };
+  auto ready = [&](int bar, int parity) { return __all_sync(0xffffffffu, wait(bars + 8 * bar, parity)); };
+  bool live = true;
+  Copier<KB, VB, DK> copier;
+  if constexpr (kPacked && SELF)
+    if (tid < 32) copier.start(c, t, packed, lane, bars);
   int slot = 0, round = 0;                      // ring stage of tile `it`, and how often the ring went round
-  for (int it = 0; it < n; ++it) {
+  for (int it = 0; live && it < n; ++it) {
     const int tile = t.begin + it, st = it & 1, ph = ((it >> 1) & 1) ^ 1;
     const uint32_t kdst = kdst0 + st * kKeyStage, vdst = vdst0 + st * 2 * kHalf;
     const uint32_t src = c.ring + slot * ring_stage_bytes(KB, VB, DK);
     const int kind = tile < t.nq + t.nf ? 1 : 2, e0 = (tile - t.nq - (kind == 2 ? t.nf : 0)) * kTile;
     const int ne = kind == 1 ? t.n_fp16 : t.n_vis;
-    if constexpr (kPacked) {
-      if constexpr (SELF)
-        if (tid < 32 && it > 0 && live) live = copier.next(c, t, lane, bars, wait);
-      if (it < packed) live = live && __all_sync(0xffffffffu, wait(bars + 8 * (kRingFull + slot), round & 1));
-    }
-    live = live && __all_sync(0xffffffffu, wait(bars + 8 * (kKEmpty + st), ph));
-    if (!live) break;
-    if (it < packed) {
-      if constexpr (kPacked) decode_keys<KB, DK, NT>(c, tid, src, src + kTile * (kRowK + kRowV), kdst);
-    } else {
-      copy_rows<KB, DK, NT>(c, true, kind, e0, ne, tid, kdst);
-    }
-    arrive(kKFull + st);
-    live = live && __all_sync(0xffffffffu, wait(bars + 8 * (kVEmpty + st), ph));
-    if (!live) break;
-    if (it < packed) {
-      if constexpr (kPacked) {
-        decode_values<VB, NT>(c, tid, src + kTile * kRowK, src + kTile * (kRowK + kRowV) + kMetaBytes / 2, vdst);
-        if (++slot == c.stages) {
-          slot = 0;
-          ++round;
-        }
+    if constexpr (kPacked && SELF)
+      if (tid < 32 && it > 0 && !copier.next(c, t, lane, bars, wait)) break;
+    if (kPacked && it < packed && !ready(kRingFull + slot, round & 1)) break;
+    if constexpr (PART != kValues) {
+      live = ready(kKEmpty + st, ph);
+      if (!live) break;
+      if (it < packed) {
+        if constexpr (kPacked) decode_keys<KB, DK, NT>(c, tid, src, src + kTile * (kRowK + kRowV), kdst);
+      } else {
+        copy_rows<KB, DK, NT>(c, true, kind, e0, ne, tid, kdst);
       }
-    } else {
-      copy_rows<VB, kTile, NT>(c, false, kind, e0, ne, tid, vdst);
+      arrive(kKFull + st);
     }
-    arrive(kVFull + st);
-    if constexpr (kPacked)
-      if (it < packed && lane == 0) mbar_arrive(bars + 8 * (kRingEmpty + (slot == 0 ? c.stages - 1 : slot - 1)));
+    if constexpr (PART != kKeys) {
+      live = ready(kVEmpty + st, ph);
+      if (!live) break;
+      if (it < packed) {
+        if constexpr (kPacked)
+          decode_values<VB, NT>(c, tid, src + kTile * kRowK, src + kTile * (kRowK + kRowV) + kMetaBytes / 2, vdst);
+      } else {
+        copy_rows<VB, kTile, NT>(c, false, kind, e0, ne, tid, vdst);
+      }
+      arrive(kVFull + st);
+    }
+    if (kPacked && it < packed) {
+      if (lane == 0) mbar_arrive(bars + 8 * (kRingEmpty + slot));
+      if (++slot == c.stages) {
+        slot = 0;
+        ++round;
+      }
+    }
   }
   if constexpr (kPacked && SELF)
-    if (tid < 32) copier.drain(c, lane, bars, live);
+    if (tid < 32) copier.drain(c, lane, bars, *wait.fail == 0);
 }
 
 // f with the cache's bit widths as constants.

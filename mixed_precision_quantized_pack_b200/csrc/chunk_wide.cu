@@ -161,7 +161,7 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
 
   const uint32_t bars = base + Lay::kBars;
   if (tid == 0) {
-    init_token_bars<kProducerThreads, MT>(bars);          // with two row tiles both streams use a tile
+    init_token_bars(bars, kProducerThreads / 32, kProducerThreads / 32, MT);   // with two row tiles both streams use a tile
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars + 8 * (kSFull + i), 1);
       ptx::mbar_init(bars + 8 * (kODone + i), 1);
@@ -192,7 +192,7 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
     with_bits(d, [&](auto kb, auto vb) {
       for (int i = 0; i < MT; ++i)
         copy_queries<kb.value, DK, kTile, kProducerThreads>(c, r0 + i * kTile, n_rows, pt, base + Lay::kQ + i * Lay::KH * kHalf);
-      produce<kb.value, vb.value, DK, kProducerThreads, true>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
+      produce<kb.value, vb.value, DK, kProducerThreads, kBoth, true>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
     });
   } else {
     const uint32_t ts = tmem + stream * kTile + lanes, to = tmem + 2 * kTile + stream * kTile + lanes;
