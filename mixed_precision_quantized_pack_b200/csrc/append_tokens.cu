@@ -61,7 +61,59 @@ __device__ __forceinline__ int key_slot(int c, int dk, int kb) {
   return pos * 2 * per + (r % half) * 2 + r / half;
 }
 
-__global__ void __launch_bounds__(kThreads)
+// Codes of 8 fp16 values, LSB first; prm(j) is (zero, 1 / scale, scale) of value j's group.  The
+// reciprocal decides all but quotients next to a half-integer, which take the division.
+template <typename P>
+__device__ __forceinline__ uint64_t chunk_codes(const uint4& raw, int bits, const P& prm) {
+  const __half2* hx = reinterpret_cast<const __half2*>(&raw);
+  const uint32_t levels = (1u << bits) - 1u;
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __half22float2(hx[e]);
+    x[2 * e] = f.x;
+    x[2 * e + 1] = f.y;
+  }
+  bool near = false;
+  uint64_t codes = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float3 p = prm(j);
+    codes |= static_cast<uint64_t>(code_fast_l(x[j], p.x, p.y, levels, near)) << (j * bits);
+  }
+  if (near) {
+    codes = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float3 p = prm(j);
+      codes |= static_cast<uint64_t>(code_exact_l(x[j], p.x, p.z, levels)) << (j * bits);
+    }
+  }
+  return codes;
+}
+
+// n bits (8, 16, 32 or 64) at bit offset `off`, a multiple of n, of a packed row.
+__device__ __forceinline__ void store_codes(uint32_t* row, int off, int n, uint64_t codes) {
+  if (n == 64) {
+    row[off / 32] = static_cast<uint32_t>(codes);
+    row[off / 32 + 1] = static_cast<uint32_t>(codes >> 32);
+  } else if (n == 32) {
+    row[off / 32] = static_cast<uint32_t>(codes);
+  } else if (n == 16) {
+    reinterpret_cast<uint16_t*>(row)[off / 16] = static_cast<uint16_t>(codes);
+  } else {
+    reinterpret_cast<uint8_t*>(row)[off / 8] = static_cast<uint8_t>(codes);
+  }
+}
+
+// Zeros in the bytes behind the last field of a width map's packed value rows.
+__device__ __forceinline__ void zero_tail(const int* cnt, int words, uint32_t* rows, int n, int tid) {
+  const int bytes = (cnt[0] * 8 + cnt[1] * 4 + cnt[2] * 2 + cnt[3]) / 8;    // groups of at least 8 channels: whole bytes
+  for (int i = tid; i < n * (4 * words - bytes); i += kThreads)
+    reinterpret_cast<uint8_t*>(rows + (i / (4 * words - bytes)) * words)[bytes + i % (4 * words - bytes)] = 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 4)
 append_groups_kernel(Dims d, CacheOut c, SeqChunk w, const __half* __restrict__ k, const __half* __restrict__ v,
                      int T, const int* __restrict__ index, int max_new_groups) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -114,24 +166,41 @@ append_groups_kernel(Dims d, CacheOut c, SeqChunk w, const __half* __restrict__ 
   }
   const int g = s.Q / d.gk + blockIdx.x;
   if (g >= Q2 / d.gk) return;
-  // shared memory: key rows, value rows, key (scale, zero), value (scale, zero), side residual sums,
+  // shared memory: key rows, value rows, key (scale, zero) and 1 / scale, slabs, side residual sums,
   // side (scale, zero)
   __half* sk = reinterpret_cast<__half*>(smem);
   __half* sv = sk + d.gk * ks;
   float2* kp = reinterpret_cast<float2*>(sv + d.gk * vs);
-  float2* vp = kp + d.dk;
-  float* y = reinterpret_cast<float*>(vp + d.gk * d.nvg);
+  float* kr = reinterpret_cast<float*>(kp + d.dk);
+  float* vp = kr + d.dk;                            // 4 KB: the slabs' extremes
+  float* y = vp + 1024;
   float2* zp = reinterpret_cast<float2*>(y + d.gk * 8);
   const int p0 = g * d.gk;
-  for (int t = warp; t < d.gk; t += nwarps) {
-    const TokenSource a = token_source(d, c.win_k, k, d.dk, index, T, s, b, bh, p0 + t);
-    const TokenSource e2 = token_source(d, c.win_v, v, d.dv, index, T, s, b, bh, p0 + t);
-    for (int e = lane; e < vk; e += 32)
-      reinterpret_cast<uint4*>(sk + t * ks)[e] = reinterpret_cast<const uint4*>(a.base)[e];
-    for (int e = lane; e < vv; e += 32)
-      reinterpret_cast<uint4*>(sv + t * vs)[e] = reinterpret_cast<const uint4*>(e2.base)[e];
-    __syncwarp();
-    if (a.fresh && d.rot) rotate_smem_row(sk + t * ks, d, lane);
+  // the group's rows, a 16-byte piece per thread and step, eight steps of loads ahead of their stores
+  {
+    constexpr int kSteps = 8;
+    const int total = d.gk * (vk + vv);
+    for (int i0 = tid; i0 < total; i0 += kSteps * kThreads) {
+      uint4 x[kSteps];
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        const int i = i0 + j * kThreads, t = i / (vk + vv), e = i % (vk + vv);
+        if (i < total)
+          x[j] = __ldg(reinterpret_cast<const uint4*>(
+                     e < vk ? token_source(d, c.win_k, k, d.dk, index, T, s, b, bh, p0 + t).base
+                            : token_source(d, c.win_v, v, d.dv, index, T, s, b, bh, p0 + t).base) + (e < vk ? e : e - vk));
+      }
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        const int i = i0 + j * kThreads, t = i / (vk + vv), e = i % (vk + vv);
+        if (i < total) reinterpret_cast<uint4*>(e < vk ? sk + t * ks : sv + t * vs)[e < vk ? e : e - vk] = x[j];
+      }
+    }
+    if (d.rot) {
+      __syncthreads();
+      for (int t = warp; t < d.gk; t += nwarps)
+        if (p0 + t >= s.L) rotate_smem_row(sk + t * ks, d, lane);        // new rows; the window's are rotated
+    }
   }
   __syncthreads();
   long long row0 = static_cast<long long>(group_row(d, c.table, b, h, g));
@@ -140,68 +209,110 @@ append_groups_kernel(Dims d, CacheOut c, SeqChunk w, const __half* __restrict__ 
       !KVQ_IN_BOUNDS(d, kSiteTokGroup, gidx, quant_groups(d)))
     row0 = gidx = 0;
 
-  // ---- (scale, zero): keys per channel, values per token and channel group ----
-  for (int i = tid; i < d.dk + d.gk * d.nvg; i += kThreads) {
-    const bool key = i < d.dk;
-    const int t = key ? 0 : (i - d.dk) / d.nvg, vg = key ? 0 : (i - d.dk) % d.nvg;
-    int width = key ? d.kb : d.vb, off;
-    if (d.var) channel_width(key ? d.kcnt : d.vcnt, key ? i : vg * d.gv, &width, &off);
+  // ---- key (scale, zero): two channels and a slab of the tokens per thread, then over the slabs ----
+  __half2* red = reinterpret_cast<__half2*>(vp);                 // [slab][channel pair][min, max]
+  const int pairs = d.dk / 2, slabs = min(kThreads / pairs, d.gk);
+  {
+    const int p = tid % pairs, slab = tid / pairs;
+    if (slab < slabs) {
+      const __half* x = sk + slab * ks + 2 * p;
+      __half2 mn = *reinterpret_cast<const __half2*>(x), mx = mn;
+      for (int t = slab + slabs; t < d.gk; t += slabs) {
+        const __half2 e = *reinterpret_cast<const __half2*>(sk + t * ks + 2 * p);
+        mn = __hmin2(mn, e);
+        mx = __hmax2(mx, e);
+      }
+      red[(slab * pairs + p) * 2] = mn;
+      red[(slab * pairs + p) * 2 + 1] = mx;
+    }
+  }
+  __syncthreads();
+  for (int ch = tid; ch < d.dk; ch += kThreads) {
+    int width = d.kb, off;
+    if (d.var) channel_width(d.kcnt, ch, &width, &off);
     GroupParams gp;
     gp.scale = gp.zero = 0.0f;
     gp.sz = __floats2half2_rn(0.0f, 0.0f);
     if (width) {
-      const __half* x = key ? sk + i : sv + t * vs + vg * d.gv;
-      const int n = key ? d.gk : d.gv, step = key ? ks : 1;
-      __half mn = x[0], mx = x[0];
-      for (int j = 1; j < n; ++j) {
-        const __half e = x[j * step];
-        mn = __hmin(mn, e);
-        mx = __hmax(mx, e);
+      const __half* r = reinterpret_cast<const __half*>(red) + (ch / 2) * 4 + ch % 2;
+      __half mn = r[0], mx = r[2];
+      for (int sl = 1; sl < slabs; ++sl) {
+        mn = __hmin(mn, r[sl * pairs * 4]);
+        mx = __hmax(mx, r[sl * pairs * 4 + 2]);
       }
       gp = group_params_b(__half2float(mn), __half2float(mx), width);
     }
-    if (key) {
-      kp[i] = make_float2(gp.scale, gp.zero);
-      __half* blk = reinterpret_cast<__half*>(c.ksz) + gidx * 2 * d.dk;
-      const int at = d.var ? 2 * i : key_slot(i, d.dk, d.kb), to_zero = d.var ? 1 : 32 / d.kb;
-      blk[at] = __low2half(gp.sz);
-      blk[at + to_zero] = __high2half(gp.sz);
-    } else {
-      vp[i - d.dk] = make_float2(gp.scale, gp.zero);
-      c.vsz[(row0 + t) * d.nvg + vg] = gp.sz;
-    }
+    kp[ch] = make_float2(gp.scale, gp.zero);
+    kr[ch] = gp.scale == 0.0f ? 0.0f : __frcp_rn(gp.scale);
+    __half* blk = reinterpret_cast<__half*>(c.ksz) + gidx * 2 * d.dk;
+    const int at = d.var ? 2 * ch : key_slot(ch, d.dk, d.kb), to_zero = d.var ? 1 : 32 / d.kb;
+    blk[at] = __low2half(gp.sz);
+    blk[at + to_zero] = __high2half(gp.sz);
   }
   __syncthreads();
 
-  // ---- codes ----
-  for (int i = tid; i < d.gk * (d.kw + d.vw); i += kThreads) {
-    const bool key = i < d.gk * d.kw;
-    const int j = key ? i : i - d.gk * d.kw;
-    const int words = key ? d.kw : d.vw, t = j / words, wd = j % words;
-    auto code = [&](int ch, int bits) {
-      const float2 sz = key ? kp[ch] : vp[t * d.nvg + ch / d.gv];
+  // ---- values: 8 channels of a token per thread, a group's threads side by side in a warp ----
+  {
+    const int tpg = d.gv / 8;                                    // threads a group: a power of two, at most 32
+    const int total = d.gk * vv;                                 // a multiple of 32: whole warps take part or none
+    for (int i = tid; i < total; i += kThreads) {
+      const int t = i / vv, cc = i % vv, vg = cc / tpg;
+      const uint4 raw = *reinterpret_cast<const uint4*>(sv + t * vs + 8 * cc);
+      const __half2* hx = reinterpret_cast<const __half2*>(&raw);
+      __half2 mn = __hmin2(__hmin2(hx[0], hx[1]), __hmin2(hx[2], hx[3]));
+      __half2 mx = __hmax2(__hmax2(hx[0], hx[1]), __hmax2(hx[2], hx[3]));
+      for (int o = 1; o < tpg; o <<= 1) {
+        mn = __hmin2(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = __hmax2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      }
+      int width = d.vb, off = 8 * cc * d.vb;
+      if (d.var) channel_width(d.vcnt, 8 * cc, &width, &off);
       GroupParams gp;
-      gp.scale = sz.x;
-      gp.zero = sz.y;
-      return quant_code_b(__half2float(key ? sk[t * ks + ch] : sv[t * vs + ch]), gp, bits);
-    };
-    uint32_t word = 0;
-    if (d.var) {
-      // a width map: the classes' channels (8, 4, 2, 1 bits) follow each other in the row; the
-      // word takes those whose field starts inside it
-      const int* cnt = key ? d.kcnt : d.vcnt;
+      gp.scale = gp.zero = 0.0f;
+      gp.sz = __floats2half2_rn(0.0f, 0.0f);
+      if (width)
+        gp = group_params_b(__half2float(__hmin(__low2half(mn), __high2half(mn))),
+                            __half2float(__hmax(__low2half(mx), __high2half(mx))), width);
+      if (cc % tpg == 0) c.vsz[(row0 + t) * d.nvg + vg] = gp.sz;
+      if (width == 0) continue;
+      const uint64_t codes = chunk_codes(raw, width, [&](int) { return make_float3(gp.zero, gp.scale == 0.0f ? 0.0f : __frcp_rn(gp.scale), gp.scale); });
+      store_codes(c.vcode + (row0 + t) * d.vw, off, 8 * width, codes);
+    }
+    if (d.var) zero_tail(d.vcnt, d.vw, c.vcode + row0 * d.vw, d.gk, tid);
+  }
+
+  // ---- key codes: 8 channels of a token per thread; of a width map, a word ----
+  if (!d.var) {
+    // d_k / 8 divides the CTA, so a thread keeps its chunk and the chunk's parameters
+    const int cc = tid % vk;
+    float3 prm[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) prm[j] = make_float3(kp[8 * cc + j].y, kr[8 * cc + j], kp[8 * cc + j].x);
+    for (int t = tid / vk; t < d.gk; t += kThreads / vk) {
+      const uint4 raw = *reinterpret_cast<const uint4*>(sk + t * ks + 8 * cc);
+      const uint64_t codes = chunk_codes(raw, d.kb, [&](int j) { return prm[j]; });
+      store_codes(c.kcode + (row0 + t) * d.kw, 8 * cc * d.kb, 8 * d.kb, codes);
+    }
+  } else {
+    for (int i = tid; i < d.gk * d.kw; i += kThreads) {
+      // the classes' channels (8, 4, 2, 1 bits) follow each other in the row; the word takes those
+      // whose field starts inside it
+      const int t = i / d.kw, wd = i % d.kw;
+      uint32_t word = 0;
       int off = -32 * wd, ch = 0;
       for (int cl = 0; cl < 4 && off < 32; ++cl) {
-        const int bits = 8 >> cl, skip = off < 0 ? min(cnt[cl], -off / bits) : 0;
+        const int bits = 8 >> cl, skip = off < 0 ? min(d.kcnt[cl], -off / bits) : 0;
         off += skip * bits;
-        const int end = ch + cnt[cl];
-        for (ch += skip; ch < end && off < 32; ++ch, off += bits) word |= code(ch, bits) << off;
+        const int end = ch + d.kcnt[cl];
+        for (ch += skip; ch < end && off < 32; ++ch, off += bits) {
+          GroupParams gp;
+          gp.scale = kp[ch].x;
+          gp.zero = kp[ch].y;
+          word |= quant_code_b(__half2float(sk[t * ks + ch]), gp, bits) << off;
+        }
       }
-    } else {
-      const int bits = key ? d.kb : d.vb, per = 32 / bits;
-      for (int e = 0; e < per; ++e) word |= code(wd * per + e, bits) << (e * bits);
+      c.kcode[(row0 + t) * d.kw + wd] = word;
     }
-    (key ? c.kcode : c.vcode)[(row0 + t) * words + wd] = word;
   }
 
   // ---- side code: the residual of every key projected on U_h, quantized per coordinate ----
@@ -250,21 +361,39 @@ append_groups_kernel(Dims d, CacheOut c, SeqChunk w, const __half* __restrict__ 
   }
 }
 
-// The new tokens that stay in the window, a warp per row: positions max(L, Q') .. L + n - 1.
+// The new tokens that stay in the window, positions max(L, Q') .. L + n - 1: kRows rows a warp, the
+// 16-byte pieces of their keys and values dealt to its lanes, all loads ahead of the stores.
+constexpr int kRows = 4;
 __global__ void __launch_bounds__(kThreads)
 append_window_kernel(Dims d, CacheOut c, SeqChunk w, const __half* __restrict__ k, const __half* __restrict__ v,
                      int T, const int* __restrict__ index) {
   const int h = blockIdx.y, b = blockIdx.z, bh = b * d.Hkv + h;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const SeqNew s = seq_new(w, b, d.log_retain);
-  const int Q2 = prefix_of(d, s.L + s.n);
-  const int p = max(s.L, Q2) + blockIdx.x * (kThreads / 32) + warp;
-  if (p >= s.L + s.n) return;
-  const __half* pk = token_source(d, nullptr, k, d.dk, index, T, s, b, bh, p).base;
-  const __half* pv = token_source(d, nullptr, v, d.dv, index, T, s, b, bh, p).base;
-  const long long row = static_cast<long long>(bh) * d.cap + p % d.cap;
-  if (!KVQ_IN_BOUNDS(d, kSiteTokWin, row, win_rows(d))) return;
-  if (d.rot) {
+  const int first = max(s.L, prefix_of(d, s.L + s.n)) + (blockIdx.x * (kThreads / 32) + warp) * kRows;
+  const int rows = min(kRows, s.L + s.n - first);
+  if (rows <= 0) return;
+  const int vk = d.rot ? 0 : d.dk / 8, vv = d.dv / 8;      // (rotated keys go row by row below)
+  for (int e = lane; e < vk + vv; e += 32) {
+    uint4 x[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (i < rows) {
+        const __half* src = e < vk ? token_source(d, nullptr, k, d.dk, index, T, s, b, bh, first + i).base + 8 * e
+                                   : token_source(d, nullptr, v, d.dv, index, T, s, b, bh, first + i).base + 8 * (e - vk);
+        x[i] = __ldg(reinterpret_cast<const uint4*>(src));
+      }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const long long row = static_cast<long long>(bh) * d.cap + (first + i) % d.cap;
+      if (i < rows && KVQ_IN_BOUNDS(d, kSiteTokWin, row, win_rows(d)))
+        *reinterpret_cast<uint4*>(e < vk ? c.win_k + row * d.dk + 8 * e : c.win_v + row * d.dv + 8 * (e - vk)) = x[i];
+    }
+  }
+  for (int i = 0; d.rot && i < rows; ++i) {
+    const __half* pk = token_source(d, nullptr, k, d.dk, index, T, s, b, bh, first + i).base;
+    const long long row = static_cast<long long>(bh) * d.cap + (first + i) % d.cap;
+    if (!KVQ_IN_BOUNDS(d, kSiteTokWin, row, win_rows(d))) continue;
     float x[8];
 #pragma unroll
     for (int m = 0; m < 8; ++m) x[m] = m < d.dk / 32 ? __half2float(pk[lane + 32 * m]) : 0.0f;
@@ -272,12 +401,7 @@ append_window_kernel(Dims d, CacheOut c, SeqChunk w, const __half* __restrict__ 
 #pragma unroll
     for (int m = 0; m < 8; ++m)
       if (m < d.dk / 32) c.win_k[row * d.dk + lane + 32 * m] = __float2half_rn(x[m]);
-  } else {
-    for (int e = lane; e < d.dk / 8; e += 32)
-      reinterpret_cast<uint4*>(c.win_k + row * d.dk)[e] = reinterpret_cast<const uint4*>(pk)[e];
   }
-  for (int e = lane; e < d.dv / 8; e += 32)
-    reinterpret_cast<uint4*>(c.win_v + row * d.dv)[e] = reinterpret_cast<const uint4*>(pv)[e];
 }
 
 }  // namespace
@@ -287,10 +411,10 @@ cudaError_t launch_append_tokens(const Dims& d, const CacheOut& c, const SeqChun
                                  cudaStream_t s) {
   if (max_new_groups > 0) {
     const size_t rows = static_cast<size_t>(d.gk) * (d.dk + d.dv + 2 * kPad) * 2;
-    size_t smem = rows + d.dk * 8 + static_cast<size_t>(d.gk) * d.nvg * 8 + d.gk * 32 + 64;
+    size_t smem = rows + d.dk * 12 + 4096 + d.gk * 32 + 64;
       smem = std::max(smem, static_cast<size_t>(kMaxRetained) * (d.dk + d.dv + 2 * kPad) * 2);
-    const cudaError_t e = cudaFuncSetAttribute(append_groups_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(append_groups_kernel, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const dim3 grid(max_new_groups + (d.log_retain ? 1 : 0), d.Hkv, d.B);
     append_groups_kernel<<<grid, kThreads, smem, s>>>(d, c, w, k, v, T, index, max_new_groups);
@@ -298,7 +422,8 @@ cudaError_t launch_append_tokens(const Dims& d, const CacheOut& c, const SeqChun
     if (e2 != cudaSuccess) return e2;
   }
   if (max_tail > 0) {
-    const dim3 grid((max_tail + kThreads / 32 - 1) / (kThreads / 32), d.Hkv, d.B);
+    const int per_cta = kThreads / 32 * kRows;
+    const dim3 grid((max_tail + per_cta - 1) / per_cta, d.Hkv, d.B);
     append_window_kernel<<<grid, kThreads, 0, s>>>(d, c, w, k, v, T, index);
     return cudaGetLastError();
   }

@@ -358,8 +358,8 @@ cudaError_t launch(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaSt
   using Lay = Layout<DK, N>;
   const int stages = ring_stages(d, Lay::kFixed);
   const int smem = Lay::kFixed + stages * ring_stage_bytes(d.kb, d.vb, d.dk);
-  const cudaError_t e =
-      cudaFuncSetAttribute(chunk_narrow_kernel<DK, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(chunk_narrow_kernel<DK, N>, smem);
   if (e != cudaSuccess) return e;
   // the softmax warps' increase waits for registers that the launch must have: checked, not assumed
   static const int regs = [] {

@@ -232,6 +232,8 @@ chunk_simple_kernel(Dims d, CacheBufs cb, const __grid_constant__ ChunkArgs a) {
 // 0 for a row that saw nothing; rows behind a sequence's new tokens are not written.
 __global__ void __launch_bounds__(128)
 chunk_combine_kernel(Dims d, const __grid_constant__ ChunkArgs a, long long rows) {
+  // a programmatic dependent of the chunk kernel: its partials are visible behind this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (row >= rows) return;
@@ -311,8 +313,16 @@ cudaError_t launch_chunk_simple(const Dims& d, const CacheBufs& c, const ChunkAr
 
 cudaError_t launch_chunk_combine(const Dims& d, const ChunkArgs& a, cudaStream_t s) {
   const long long rows = static_cast<long long>(d.B) * d.Hq * a.T;
-  chunk_combine_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(d, a, rows);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_combine_kernel, d, a, rows);
 }
 
 cudaError_t launch_rotate_rows(const Dims& d, const __half* src, __half* dst, long long rows, float inv_c,

@@ -404,7 +404,8 @@ template <int DK, int MT>
 cudaError_t launch(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s) {
   const int stages = ring_stages(d, Layout<DK, MT>::kFixed);
   const int smem = Layout<DK, MT>::kFixed + stages * ring_stage_bytes(d.kb, d.vb, d.dk);
-  const cudaError_t e = cudaFuncSetAttribute(chunk_wide_kernel<DK, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(chunk_wide_kernel<DK, MT>, smem);
   if (e != cudaSuccess) return e;
   const int row_blocks = (d.n_rep * a.T + MT * kTile - 1) / (MT * kTile);
   chunk_wide_kernel<DK, MT><<<dim3(a.splits * row_blocks, d.Hkv, d.B), kThreads, smem, s>>>(d, c, a, stages);

@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <memory>
 #include <new>
 #include <vector>
 
@@ -1290,8 +1291,8 @@ int kvq_compact_pages(kvq_cache* c, int end, void* stream) {
     std::vector<int> from, to(d.n_pages, -1);
     for (int p = 0; p < d.n_pages; ++p)
       if (c->refs[p] > 0 && (p < lo || p >= hi)) from.push_back(p);
-    std::vector<kvq::PageMoves> batch(1);
-    kvq::PageMoves& m = batch[0];
+    const std::unique_ptr<kvq::PageMoves> batch(new kvq::PageMoves);
+    kvq::PageMoves& m = *batch;
     DeviceScope on(c->device);
     if (!on.ok) return KVQ_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1307,7 +1308,7 @@ int kvq_compact_pages(kvq_cache* c, int end, void* stream) {
       m.src[m.n_moves] = from[next];
       m.dst[m.n_moves] = p;
       to[from[next++]] = p;
-      if (++m.n_moves == kvq::PageMoves::kCap) {
+      if (++m.n_moves == kvq::kMostMoves) {
         const int rc = flush();
         if (rc) return rc;
       }
@@ -1318,7 +1319,7 @@ int kvq_compact_pages(kvq_cache* c, int end, void* stream) {
         if (to[c->table[idx]] < 0) continue;
         m.idx[m.n_writes] = static_cast<int>(idx);
         m.page[m.n_writes] = to[c->table[idx]];
-        if (++m.n_writes == kvq::PageMoves::kCap) {
+        if (++m.n_writes == kvq::kMostMoves) {
           const int rc = flush();
           if (rc) return rc;
         }

@@ -74,7 +74,9 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(Dims d, CacheOut c, Fork
 }
 
 // grid (moves + CTAs for the table entries, parts): CTA x < n_moves copies page src[x].
-__global__ void __launch_bounds__(kThreads) page_moves_kernel(Dims d, CacheOut c, const __grid_constant__ PageMoves m) {
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+page_moves_kernel(Dims d, CacheOut c, const __grid_constant__ PageMovesT<CAP> m) {
   const int x = blockIdx.x;
   if (x >= m.n_moves) {
     const int i = (x - m.n_moves) * kThreads + threadIdx.x;
@@ -122,7 +124,18 @@ cudaError_t launch_page_moves(const Dims& d, const CacheOut& c, const PageMoves&
   if (m.n_moves + table_ctas == 0) return cudaSuccess;
   const int want = m.n_moves ? (8 * d.sm_count + m.n_moves - 1) / m.n_moves : 1;
   const dim3 grid(m.n_moves + table_ctas, std::max(1, std::min(want, 8)));
-  page_moves_kernel<<<grid, kThreads, 0, s>>>(d, c, m);
+  if (m.n_moves <= kFewMoves && m.n_writes <= kFewMoves) {
+    PageMovesT<kFewMoves> f;
+    f.n_moves = m.n_moves;
+    f.n_writes = m.n_writes;
+    std::copy_n(m.src, m.n_moves, f.src);
+    std::copy_n(m.dst, m.n_moves, f.dst);
+    std::copy_n(m.idx, m.n_writes, f.idx);
+    std::copy_n(m.page, m.n_writes, f.page);
+    page_moves_kernel<kFewMoves><<<grid, kThreads, 0, s>>>(d, c, f);
+  } else {
+    page_moves_kernel<kMostMoves><<<grid, kThreads, 0, s>>>(d, c, m);
+  }
   return cudaGetLastError();
 }
 

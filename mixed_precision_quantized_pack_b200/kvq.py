@@ -394,6 +394,7 @@ class KVCache:
         self.device = torch.device(device or "cuda")
         self.sizes = kvq_buffer_sizes(self.cfg)
         self.buffers: Dict[str, Optional[torch.Tensor]] = {}
+        self._views: Dict[str, torch.Tensor] = {}      # typed views of the buffers, made once
         for n in POINTER_FIELDS:
             sz = self.sizes[n]
             self.buffers[n] = torch.zeros(sz, dtype=torch.uint8, device=self.device) if sz else None
@@ -470,13 +471,13 @@ class KVCache:
 
     # several tokens per sequence, whole sequences: these run on the cache's own device
     def _on_device(self, stream):
-        return _stream(torch.cuda.current_stream(self.view("win_k").device) if stream is None else stream)
+        return _stream(torch.cuda.current_stream(self.workspace.device) if stream is None else stream)
 
     def _new_tokens(self, k_new: torch.Tensor, v_new: torch.Tensor, counts):
         c = self.cfg
         if k_new.dim() != 4:
             raise ValueError("k_new: need [batch][n_kv_heads][T][d_k]")
-        T, dev = k_new.shape[2], self.view("win_k").device
+        T, dev = k_new.shape[2], self.workspace.device
         _fp16_cuda(k_new, (c["batch"], c["n_kv_heads"], T, c["d_k"]), "k_new")
         _fp16_cuda(v_new, (c["batch"], c["n_kv_heads"], T, c["d_v"]), "v_new")
         if k_new.device != dev or v_new.device != dev:
@@ -503,21 +504,28 @@ class KVCache:
         if mask is not None:
             _int32_cuda(mask, (c["batch"], T, -(-T // 32)), dev, "mask")
         shape = (c["batch"], c["n_q_heads"], T, c["d_v"])
-        # what is allocated here belongs to the stream that the kernels run on
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        s = s if hasattr(s, "cuda_stream") else torch.cuda.ExternalStream(int(s), device=dev)
+        if stream is None:
+            return self._chunk(q, k_new, v_new, counts, mask, out, shape, num_splits,
+                               torch.cuda.current_stream(dev))
+        # what is allocated for the call belongs to the stream that the kernels run on
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
         with torch.cuda.stream(s):
-            if out is None:
-                partly = counts is not None and min(counts) < T
-                out = (torch.zeros if partly else torch.empty)(shape, dtype=torch.float16, device=dev)
-            _fp16_cuda(out, shape, "out")
-            if q.device != dev or out.device != dev:
-                raise ValueError(f"q, out: need tensors on the cache's device {dev}")
-            n = kvq_chunk_workspace_size(self.handle, T, num_splits)
-            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+            return self._chunk(q, k_new, v_new, counts, mask, out, shape, num_splits, s)
+
+    def _chunk(self, q, k_new, v_new, counts, mask, out, shape, num_splits, stream):
+        T, dev = shape[2], self.workspace.device
+        if out is None:
+            partly = counts is not None and min(counts) < T
+            out = (torch.zeros if partly else torch.empty)(shape, dtype=torch.float16, device=dev)
+        _fp16_cuda(out, shape, "out")
+        if q.device != dev or out.device != dev:
+            raise ValueError(f"q, out: need tensors on the cache's device {dev}")
+        n = kvq_chunk_workspace_size(self.handle, T, num_splits)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         kvq_chunk_attention(self.handle, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), T, counts,
                             mask.data_ptr() if mask is not None else None, out.data_ptr(),
-                            ws.data_ptr() if n else None, n, num_splits, self.workspace.data_ptr(), _stream(s))
+                            ws.data_ptr() if n else None, n, num_splits, self.workspace.data_ptr(),
+                            stream.cuda_stream)
         return out
 
     def append_tokens(self, k_new: torch.Tensor, v_new: torch.Tensor, counts=None,
@@ -581,6 +589,11 @@ class KVCache:
 
     # typed views of the buffers, in the layouts of include/kvq.h
     def view(self, name: str) -> torch.Tensor:
+        if name not in self._views:
+            self._views[name] = self._typed_view(name)
+        return self._views[name]
+
+    def _typed_view(self, name: str) -> torch.Tensor:
         c = self.cfg
         B, H, dk, dv = c["batch"], c["n_kv_heads"], c["d_k"], c["d_v"]
         kb, vb, gk, gv = c["k_bits"], c["v_bits"], c["group_k"], c["group_v"]
