@@ -83,6 +83,22 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// The streams take turns at the exponentials (every tile: 128 of a row, a thread's longest stretch and
+// the special-function unit's).  Side by side they would both crawl through them and then both wait
+// for the tensor core; in turn one computes weights while the other's products run.
+__device__ __forceinline__ void turn_take(int stream) {
+  if (stream == 0)
+    asm volatile("bar.sync 5, 256;" ::: "memory");
+  else
+    asm volatile("bar.sync 6, 256;" ::: "memory");
+}
+__device__ __forceinline__ void turn_pass(int stream) {
+  if (stream == 0)
+    asm volatile("bar.arrive 6, 256;" ::: "memory");
+  else
+    asm volatile("bar.arrive 5, 256;" ::: "memory");
+}
+
 // The scores of 64 columns that a row does not see become -inf.
 __device__ __forceinline__ void mask64(uint32_t (&x)[64], uint32_t see0, uint32_t see1) {
 #pragma unroll
@@ -203,6 +219,7 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
     const int first = MT == 2 ? 0 : stream;
     const bool issuer = (warp & 3) == 0;       // the stream's first warp
     const bool idle = !__any_sync(0xffffffffu, row_ok);       // no row of the warp counts: P may be anything
+    if (stream == 1) turn_pass(1);          // stream 0 begins
     bool live = true;
     // S of the stream's tile `it`, once its keys are there
     auto score = [&](int it) {
@@ -222,16 +239,17 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
       // a wait that runs out ends the work, not the loop: the stream's barrier counts every warp
       live = live && __all_sync(0xffffffffu, wait(bars + 8 * (kSFull + stream), mine & 1));
       fence_after();
+      bool full = true;
+      uint32_t see[4];                       // columns of the tile the row sees, 32 a word (unless `full`)
       if (live && !idle) {
-        // columns of the tile this row sees, 32 a word
         const int tile = t.begin + it;
         const int kind = tile < t.nq ? 0 : tile < t.nq + t.nf ? 1 : 2;
         const int e0 = (tile - (kind > 0 ? t.nq : 0) - (kind > 1 ? t.nf : 0)) * kTile;
         const int nv = (kind == 0 ? s.Q : kind == 1 ? t.n_fp16 : t.n_vis) - e0;
         // retained tokens of a quantized tile are read from the fp16 list
-        unsigned hits = kind == 0 ? __ballot_sync(0xffffffffu, ret_pos >= e0 && ret_pos < e0 + kTile) : 0u;
-        bool full = nv >= kTile && hits == 0 && kind != 2;
-        uint32_t see[4];
+        unsigned hits = 0u;
+        if (kind == 0 && s.n_ret) hits = __ballot_sync(0xffffffffu, ret_pos >= e0 && ret_pos < e0 + kTile);
+        full = nv >= kTile && hits == 0 && kind != 2;
         if (!full) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) see[c] = below(nv - 32 * c);
@@ -254,6 +272,8 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
             full = __all_sync(0xffffffffu, (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu);
           }
         }
+      }
+      if (live && !idle) {
         float mx = -INFINITY;
 #pragma unroll 1
         for (int h2 = 0; h2 < 2; ++h2) {      // loops, not copies: the roles' code shares an instruction cache
@@ -264,10 +284,10 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
           mx = max64(x, mx);
         }
         const float m_new = mx * alpha;
-        if (__any_sync(0xffffffffu, m_new > m_ref + kLazy)) {
-          const float m2 = fmaxf(m_ref, m_new);
-          const float f = m2 == -INFINITY ? 1.0f : ptx::ex2(m_ref - m2);
-          m_ref = m2;
+        const bool mv = m_new > m_ref + kLazy;
+        if (__any_sync(0xffffffffu, mv)) {
+          const float f = mv ? ptx::ex2(m_ref - m_new) : 1.0f;
+          if (mv) m_ref = m_new;
           l *= f;
           // S of this tile is committed behind the stream's last P V, so O is complete
           if (mine > 0) {
@@ -282,6 +302,9 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
             }
           }
         }
+      }
+      turn_take(stream);
+      if (live && !idle) {
         const float off = kBias - (m_ref == -INFINITY ? 0.0f : m_ref);
         // the weights of a half's columns go to 32 columns whose scores have been read
 #pragma unroll 1
@@ -294,6 +317,7 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
         }
         tmem_wait_st();
       }
+      turn_pass(stream);
       fence_before();
       if (stream == 0)
         asm volatile("bar.sync 2, 128;" ::: "memory");
