@@ -150,7 +150,7 @@ chunk_narrow_kernel(const __grid_constant__ Dims d, const __grid_constant__ Cach
   const uint32_t to = tmem + 2 * N + lanes;
 
   const Ctx c{d, cb, a, s, b, h, bh, __ffs(d.gk) - 1, __ffs(d.gv) - 1, __ffs(d.nvg) - 1,
-              base + Lay::kRing, base + Lay::kPages, stages};
+              base + Lay::kRing, base + Lay::kPages, stages, ring_stage_bytes(d)};
   constexpr int kCopyWarp = (kSoftmaxThreads + 2 * Lay::NT) / 32, kMmaWarp = kCopyWarp + 1;
   if (warp == kCopyWarp) {
     with_bits(d, [&](auto kb, auto vb) {
@@ -357,7 +357,7 @@ template <int DK, int N>
 cudaError_t launch(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s) {
   using Lay = Layout<DK, N>;
   const int stages = ring_stages(d, Lay::kFixed);
-  const int smem = Lay::kFixed + stages * ring_stage_bytes(d.kb, d.vb, d.dk);
+  const int smem = Lay::kFixed + stages * ring_stage_bytes(d);
   static SmemLimit limit;
   const cudaError_t e = limit.raise(chunk_narrow_kernel<DK, N>, smem);
   if (e != cudaSuccess) return e;

@@ -1087,8 +1087,8 @@ int check_counts(const kvq_cache* c, int T, const int* counts) {
 
 // How a chunk attention runs: its split count and its workspace.
 struct ChunkPlan {
-  bool tensor;                          // the tensor-core kernel
-  int splits;
+  enum { kSimple, kTile, kFew } kernel;
+  int splits, splits_q;                 // partials per row; of those over the quantized groups (kFew)
   size_t ml, o, rot_q, rot_k, bytes;   // offsets of the workspace's parts, and its size
 };
 
@@ -1099,8 +1099,27 @@ int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
   if (rows >= (1LL << 31) || static_cast<long long>(d.Hq) * T >= (1LL << 24)) return KVQ_ERR_UNSUPPORTED;
   int longest = 0;
   for (int b = 0; b < d.B; ++b) longest = std::max(longest, c->L[b]);
-  p->tensor = c->kernel != KVQ_KERNEL_GENERIC && kvq::chunk_mma_supported(d);
-  p->splits = (p->tensor ? kvq::chunk_mma_splits : kvq::chunk_simple_splits)(d, longest, T, num_splits);
+  p->kernel = ChunkPlan::kSimple;
+  if (c->kernel != KVQ_KERNEL_GENERIC)
+    p->kernel = kvq::chunk_few_supported(d, T) ? ChunkPlan::kFew : kvq::chunk_mma_supported(d) ? ChunkPlan::kTile : ChunkPlan::kSimple;
+  p->splits_q = 0;
+  if (p->kernel == ChunkPlan::kFew) {
+    // the decode planner's split counts, the new tokens behind the fp16 list
+    int nG = 0, nF = 0;
+    for (int b = 0; b < d.B; ++b) {
+      int g, f;
+      seq_counts(d, c->L[b], &g, &f);
+      nG = std::max(nG, g);
+      nF = std::max(nF, f + T);
+    }
+    kvq_plan plan;
+    const int rc = plan_counts(d, nG, nF, c->sm_count, num_splits, true, &plan);
+    if (rc) return rc;
+    p->splits_q = plan.splits_quant;
+    p->splits = plan.splits_quant + plan.splits_fp16;
+  } else {
+    p->splits = (p->kernel == ChunkPlan::kTile ? kvq::chunk_mma_splits : kvq::chunk_simple_splits)(d, longest, T, num_splits);
+  }
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1154,6 +1173,7 @@ int kvq_chunk_attention(kvq_cache* c, const void* q, const void* k_new, const vo
   char* ws = static_cast<char*>(workspace);
   a.T = T;
   a.splits = p.splits;
+  a.splits_q = p.splits_q;
   a.score_scale = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(d.dk)));
   a.q = static_cast<const __half*>(q);
   a.k_new = static_cast<const __half*>(k_new);
@@ -1174,7 +1194,9 @@ int kvq_chunk_attention(kvq_cache* c, const void* q, const void* k_new, const vo
     a.k_new = rk;
   }
   const kvq::CacheBufs cb = cache_bufs(c);
-  rc = check_cuda((p.tensor ? kvq::launch_chunk_mma : kvq::launch_chunk_simple)(d, cb, a, s));
+  rc = check_cuda((p.kernel == ChunkPlan::kFew    ? kvq::launch_chunk_few
+                   : p.kernel == ChunkPlan::kTile ? kvq::launch_chunk_mma
+                                                  : kvq::launch_chunk_simple)(d, cb, a, s));
   if (!rc && a.splits > 1) rc = check_cuda(kvq::launch_chunk_combine(d, a, s));
   return rc;
 }

@@ -108,7 +108,7 @@ cudaError_t launch_page_moves(const Dims& d, const CacheOut& c, const PageMoves&
 struct ChunkArgs {
   SeqChunk seq;
   int T;                  // query rows per head, and rows per head of k_new / v_new
-  int splits;
+  int splits, splits_q;   // all of them; of those over the quantized groups (few-row kernel)
   float score_scale;      // log2(e) / sqrt(d_k)
   const __half* q;        // [B][Hq][T][dk], rotated when the keys are
   const __half* k_new;    // [B][Hkv][T][dk], likewise
@@ -125,6 +125,9 @@ struct ChunkArgs {
 int chunk_simple_splits(const Dims& d, int L, int T, int num_splits);
 int chunk_mma_splits(const Dims& d, int L, int T, int num_splits);
 bool chunk_mma_supported(const Dims& d);
+// One or a few new tokens, up to 16 query rows of a kv head (chunk_few.cuh).
+bool chunk_few_supported(const Dims& d, int T);
+cudaError_t launch_chunk_few(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s);
 // Up to this many query rows of a kv head the tokens take the MMA's rows (chunk_narrow.cu); with 64
 // rows the narrow kernel's softmax took 1.40 ms where the wide one takes 0.89 (32 sequences of 32k).
 constexpr int kNarrowRows = 32;
