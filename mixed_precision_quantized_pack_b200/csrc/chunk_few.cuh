@@ -48,8 +48,8 @@ struct Smem {
 
 template <int KB, int VB, int DK, int GV, int GK, int NT>
 struct Rings {
-  // three CTAs an SM with two n-tiles (their accumulators need the registers), four with one
-  static constexpr int CTAS = NT == 1 ? 4 : 3;
+  // four CTAs an SM with one n-tile, two with two: their accumulators spill at 168 registers
+  static constexpr int CTAS = NT == 1 ? 4 : 2;
   static constexpr int AVAIL = 233472 / CTAS - 1024;
   static constexpr int HDR = Smem<DK / 16, NT>::kStages;
   static constexpr int STAGE_Q = mma::quant_stage_bytes<KB, VB, DK, GV, GK, 0, 4>();
@@ -151,14 +151,16 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   constexpr float kMid = static_cast<float>(1 << (VB - 1));   // centre of the value codes
   const float alpha24 = a.score_scale * 16777216.0f;          // undoes the 2^-24 of subnormal codes
 
-  // Moves the references of an n-tile's rows where a score passes them by more than the lag allowed.
+  // Moves the references of an n-tile's rows to their maxima.  They do not lag behind: weights stay at
+  // most 1, and their products with a value scale, rounded to fp16 below, within its range (a lag
+  // of 8 measured 4% less time at most).
   auto rescale = [&](int nt, float g0, float g1) {
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       g0 = fmaxf(g0, __shfl_xor_sync(0xffffffffu, g0, o));
       g1 = fmaxf(g1, __shfl_xor_sync(0xffffffffu, g1, o));
     }
-    const bool mv0 = g0 > m_run[nt][0] + mma::kLazyRescale, mv1 = g1 > m_run[nt][1] + mma::kLazyRescale;
+    const bool mv0 = g0 > m_run[nt][0], mv1 = g1 > m_run[nt][1];
     if (__any_sync(0xffffffffu, mv0 || mv1)) {
       const float f0 = mv0 ? ptx::ex2(m_run[nt][0] - g0) : 1.0f, f1 = mv1 ? ptx::ex2(m_run[nt][1] - g1) : 1.0f;
       if (mv0) m_run[nt][0] = g0;

@@ -8,7 +8,7 @@
 //   O^T += V^T P^T   A = the decoded values (MN-major: no transposition), B = the weights, written
 //                    to shared memory by the softmax threads, a token per 128-byte row.
 //
-// Roles: 8 warps decode the tiles' keys and 8 their values (see chunk_tile.cuh), one warp copies packed tiles, one
+// Roles: 8 producer warps decode token tiles (see chunk_tile.cuh), one warp copies packed tiles, one
 // issues the MMAs (the scores of the next tile before the product of this one); four softmax warps
 // own a token (a TMEM lane) per thread and all its N scores.  A row's maximum runs over threads, so
 // it is not taken at all in the common case: the weights are formed with the reference of the
@@ -28,15 +28,13 @@ namespace {
 using namespace chunk;
 
 constexpr int kSoftmaxThreads = 128;
-// Registers: launched with 80 a thread; the softmax warps take 128, the producers give down to 64.
-constexpr int kLaunchRegs = 80, kSoftmaxRegs = 128, kProducerRegs = 64;
 constexpr float kNone = -1e30f;               // the reference of a row that has seen no token
 constexpr float kOver = kLazy + kBias;        // (references are kept with kBias taken off)
 
 template <int DK, int N>
 struct Layout {
-  static constexpr int NT = 256;                          // producer threads of the keys, and of the values
-  static constexpr int kThreads = kSoftmaxThreads + 2 * NT + 128;   // (and a warpgroup with the copying and the issuing warp)
+  static constexpr int NT = 256;                          // producer threads
+  static constexpr int kThreads = kSoftmaxThreads + NT + 64;   // and a warp that copies, one that issues the MMAs
   static constexpr int KH = DK > 64 ? DK / 64 : 1;
   static constexpr int kK = 0;
   static constexpr int kV = kK + 2 * KH * kHalf;
@@ -124,7 +122,7 @@ chunk_narrow_kernel(const __grid_constant__ Dims d, const __grid_constant__ Cach
   float* sm_w = reinterpret_cast<float*>(sm_t + N);             // [4][N] per warp: maxima, in the end sums
   const uint32_t bars = base + Lay::kBars;
   if (tid == 0) {
-    init_token_bars(bars, Lay::NT / 32, 2 * Lay::NT / 32, 1);
+    init_token_bars(bars, Lay::NT / 32, Lay::NT / 32, 1);
     for (int i = 0; i < 2; ++i) ptx::mbar_init(bars + 8 * (kSFull + i), 1);
     ptx::mbar_init(bars + 8 * kPFull, kSoftmaxThreads / 32);
     ptx::mbar_init(bars + 8 * kPvDone, 1);
@@ -144,15 +142,13 @@ chunk_narrow_kernel(const __grid_constant__ Dims d, const __grid_constant__ Cach
   fence_after();
   const uint32_t tmem = sm_tmem;
   const Waiter wait{&sm_fail};
-  static_assert(kSoftmaxThreads * kSoftmaxRegs + 2 * Lay::NT * kProducerRegs + 128 * kLaunchRegs <= Lay::kThreads * kLaunchRegs,
-                "the roles' registers fit the launch's");
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t to = tmem + 2 * N + lanes;
 
-  const Ctx c{d, cb, a, s, b, h, bh, __ffs(d.gk) - 1, __ffs(d.gv) - 1, __ffs(d.nvg) - 1,
-              base + Lay::kRing, base + Lay::kPages, stages, ring_stage_bytes(d)};
-  constexpr int kCopyWarp = (kSoftmaxThreads + 2 * Lay::NT) / 32, kMmaWarp = kCopyWarp + 1;
+  constexpr int kCopyWarp = (kSoftmaxThreads + Lay::NT) / 32, kMmaWarp = kCopyWarp + 1;
   if (warp == kCopyWarp) {
+    const Ctx c{d, cb, a, s, b, h, bh, __ffs(d.gk) - 1, __ffs(d.gv) - 1, __ffs(d.nvg) - 1,
+                base + Lay::kRing, base + Lay::kPages, stages};
     with_bits(d, [&](auto kb, auto vb) {
       if constexpr (kb.value != 16) copy_tiles<kb.value, vb.value, DK>(c, t, lane, bars, wait);
     });
@@ -197,22 +193,16 @@ chunk_narrow_kernel(const __grid_constant__ Dims d, const __grid_constant__ Cach
     __syncwarp();
     if (!ptx::mbar_wait_bounded(bars + 8 * kDone, 0, kWaitNs)) *wait.fail = 1;
     __syncthreads();
-  } else if (warp > kMmaWarp) {
-    __syncthreads();                          // two idle warps fill the warpgroup
-  } else if (warp >= kSoftmaxThreads / 32) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+  } else if (tid >= kSoftmaxThreads) {
+    const Ctx c{d, cb, a, s, b, h, bh, __ffs(d.gk) - 1, __ffs(d.gv) - 1, __ffs(d.nvg) - 1,
+                base + Lay::kRing, base + Lay::kPages, stages};
     const int pt = tid - kSoftmaxThreads;
     with_bits(d, [&](auto kb, auto vb) {
-      if (pt < Lay::NT) {
-        copy_queries<kb.value, DK, N, Lay::NT>(c, r0, n_rows, pt, base + Lay::kQ);
-        produce<kb.value, vb.value, DK, Lay::NT, kKeys, false>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
-      } else {
-        produce<kb.value, vb.value, DK, Lay::NT, kValues, false>(c, t, pt - Lay::NT, base + Lay::kK, base + Lay::kV, bars, wait);
-      }
+      copy_queries<kb.value, DK, N, Lay::NT>(c, r0, n_rows, pt, base + Lay::kQ);
+      produce<kb.value, vb.value, DK, Lay::NT, false>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
     });
     __syncthreads();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     float l[N];                               // the thread's share of the row sums
 #pragma unroll
     for (int r = 0; r < N; ++r) l[r] = 0.0f;
@@ -357,16 +347,10 @@ template <int DK, int N>
 cudaError_t launch(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s) {
   using Lay = Layout<DK, N>;
   const int stages = ring_stages(d, Lay::kFixed);
-  const int smem = Lay::kFixed + stages * ring_stage_bytes(d);
+  const int smem = Lay::kFixed + stages * ring_stage_bytes(d.kb, d.vb, d.dk);
   static SmemLimit limit;
   const cudaError_t e = limit.raise(chunk_narrow_kernel<DK, N>, smem);
   if (e != cudaSuccess) return e;
-  // the softmax warps' increase waits for registers that the launch must have: checked, not assumed
-  static const int regs = [] {
-    cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, chunk_narrow_kernel<DK, N>) == cudaSuccess ? at.numRegs : 0;
-  }();
-  if (regs != kLaunchRegs) return cudaErrorLaunchOutOfResources;
   const int row_blocks = (d.n_rep * a.T + N - 1) / N;
   chunk_narrow_kernel<DK, N><<<dim3(a.splits * row_blocks, d.Hkv, d.B), Lay::kThreads, smem, s>>>(d, c, a, stages);
   return cudaGetLastError();

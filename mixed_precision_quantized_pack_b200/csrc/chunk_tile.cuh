@@ -33,6 +33,7 @@ namespace chunk {
 constexpr int kTile = 128;                    // tokens per tile; also the value channels
 constexpr int kHalf = kTile * 128;            // bytes of 128 rows of 64 fp16 channels
 constexpr int kMaxRing = 4;                   // stages of the packed ring, at most
+constexpr int kMetaBytes = 4096;              // (scale, zero) of a tile: keys 2 KB, values 2 KB
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLazy = 8.0f;                 // log2 units the reference maximum may lag
 constexpr float kBias = 7.0f;                 // weights are 2^(s - m + kBias) < 2^15
@@ -265,14 +266,12 @@ struct Ctx {
   int b, h, bh;
   int lgk, lgv, lnvg;         // log2 of the group sizes and of the value groups per token
   uint32_t ring, pages;       // shared memory: the packed ring, the pages of the next tile to copy (16 bytes)
-  int stages, stage;          // of the ring: how many, and bytes of one
+  int stages;                 // of the ring
 };
 
 // A stage of the packed ring: key codes, value codes, key (scale, zero) blocks, value (scale, zero).
-__host__ __device__ inline int key_meta_bytes(const Dims& d) { return kTile / d.gk * d.dk * 4; }
-__host__ __device__ inline int value_meta_bytes(const Dims& d) { return kTile * d.nvg * 4; }
-__host__ __device__ inline int ring_stage_bytes(const Dims& d) {
-  return d.kb == 16 ? 0 : kTile * (d.dk * d.kb + kTile * d.vb) / 8 + key_meta_bytes(d) + value_meta_bytes(d);
+__host__ __device__ constexpr int ring_stage_bytes(int kb, int vb, int dk) {
+  return kb == 16 ? 0 : kTile * (dk * kb + kTile * vb) / 8 + kMetaBytes;
 }
 
 // The thread's codes of the key tile in the ring stage `src` to fp16 rows at `dst`.
@@ -520,7 +519,7 @@ enum TokenBars { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kRingFull = 8
 // The stages of a packed ring that fit beside `used` bytes of shared memory.
 constexpr int kMaxSmem = 232448 - 64;           // dynamic, beside the kernels' few static bytes
 inline int ring_stages(const Dims& d, int used) {
-  const int bytes = ring_stage_bytes(d);
+  const int bytes = ring_stage_bytes(d.kb, d.vb, d.dk);
   return bytes == 0 ? 0 : std::min(kMaxRing, (kMaxSmem - used) / bytes);
 }
 
@@ -528,9 +527,11 @@ inline int ring_stages(const Dims& d, int used) {
 // stage, and the values behind it, whose weights are 0, have to be finite.  By all threads of the
 // CTA, before the barrier in front of the roles.
 __device__ __forceinline__ void clear_ring(const Dims& d, uint32_t ring, int stages, int tid, int threads) {
-  const int bytes = ring_stage_bytes(d), tail = value_meta_bytes(d), pieces = tail / 16;
-  for (int i = tid; i < stages * pieces; i += threads)
-    st_shared(ring + i / pieces * bytes + bytes - tail + i % pieces * 16, make_uint4(0, 0, 0, 0));
+  const int bytes = ring_stage_bytes(d.kb, d.vb, d.dk);
+  for (int i = tid; i < stages * (kMetaBytes / 32); i += threads) {
+    const int st = i / (kMetaBytes / 32), e = i % (kMetaBytes / 32);
+    st_shared(ring + st * bytes + bytes - kMetaBytes / 2 + e * 16, make_uint4(0, 0, 0, 0));
+  }
   ptx::fence_proxy_async_smem();
 }
 
@@ -557,7 +558,7 @@ __device__ __forceinline__ void copy_tile(const Ctx& c, int tile, int slot, int 
   constexpr int kRowK = DK * KB / 8, kRowV = kTile * VB / 8;
   const int g0 = (tile * kTile) >> c.lgk, groups = min(kTile >> c.lgk, (c.s.Q >> c.lgk) - g0);
   const uint32_t bar = bars + 8 * (kRingFull + slot);
-  const uint32_t dst = c.ring + slot * c.stage;
+  const uint32_t dst = c.ring + slot * ring_stage_bytes(KB, VB, DK);
   const uint32_t kbytes = d.gk * kRowK, vbytes = d.gk * kRowV, zbytes = (d.gk << c.lnvg) * 4;
   const char* kc = reinterpret_cast<const char*>(c.cb.kcode);
   const char* vc = reinterpret_cast<const char*>(c.cb.vcode);
@@ -567,7 +568,7 @@ __device__ __forceinline__ void copy_tile(const Ctx& c, int tile, int slot, int 
     ptx::bulk_g2s(dst + i * kbytes, kc + gidx * kbytes, n * kbytes, bar);
     ptx::bulk_g2s(dst + kTile * (kRowK + kRowV) + i * (DK * 4), km + gidx * (DK * 4), n * (DK * 4), bar);
     ptx::bulk_g2s(dst + kTile * kRowK + i * vbytes, vc + gidx * vbytes, n * vbytes, bar);
-    ptx::bulk_g2s(dst + c.stage - value_meta_bytes(d) + i * zbytes, vm + gidx * zbytes, n * zbytes, bar);
+    ptx::bulk_g2s(dst + kTile * (kRowK + kRowV) + kMetaBytes / 2 + i * zbytes, vm + gidx * zbytes, n * zbytes, bar);
   };
   if (d.paged) ptx::cp_async_wait_all();          // the tile's pages
   __syncwarp();
@@ -639,10 +640,9 @@ __device__ __forceinline__ void copy_tiles(const Ctx& c, const Tiles& t, int lan
 }
 
 // The loop of NT producer threads: tiles t.begin .. t.end of the CTA into stages 0, 1, 0, ... of K and
-// V.  PART: both, or the keys or the values alone (two groups of producers, whose waits then
-// overlap with the other's decoding).  SELF: the first warp copies the packed tiles as well.
-enum Part { kBoth, kKeys, kValues };
-template <int KB, int VB, int DK, int NT, Part PART, bool SELF>
+// V.  SELF: the first warp copies the packed tiles as well.  (Two groups of 256, one for the keys
+// and one for the values, gained 6% with 16 queries and lost 11% with 32.)
+template <int KB, int VB, int DK, int NT, bool SELF>
 __device__ __forceinline__ void produce(const Ctx& c, const Tiles& t, int tid, uint32_t kdst0, uint32_t vdst0,
                                         uint32_t bars, const Waiter& wait) {
   constexpr int kKeyStage = (DK > 64 ? DK / 64 : 1) * kHalf;
@@ -665,33 +665,28 @@ __device__ __forceinline__ void produce(const Ctx& c, const Tiles& t, int tid, u
   for (int it = 0; live && it < n; ++it) {
     const int tile = t.begin + it, st = it & 1, ph = ((it >> 1) & 1) ^ 1;
     const uint32_t kdst = kdst0 + st * kKeyStage, vdst = vdst0 + st * 2 * kHalf;
-    const uint32_t src = c.ring + slot * c.stage;
+    const uint32_t src = c.ring + slot * ring_stage_bytes(KB, VB, DK);
     const int kind = tile < t.nq + t.nf ? 1 : 2, e0 = (tile - t.nq - (kind == 2 ? t.nf : 0)) * kTile;
     const int ne = kind == 1 ? t.n_fp16 : t.n_vis;
     if constexpr (kPacked && SELF)
       if (tid < 32 && it > 0 && !copier.next(c, t, lane, bars, wait)) break;
     if (kPacked && it < packed && !ready(kRingFull + slot, round & 1)) break;
-    if constexpr (PART != kValues) {
-      live = ready(kKEmpty + st, ph);
-      if (!live) break;
-      if (it < packed) {
-        if constexpr (kPacked) decode_keys<KB, DK, NT>(c, tid, src, src + kTile * (kRowK + kRowV), kdst);
-      } else {
-        copy_rows<KB, DK, NT>(c, true, kind, e0, ne, tid, kdst);
-      }
-      arrive(kKFull + st);
+    live = ready(kKEmpty + st, ph);
+    if (!live) break;
+    if (it < packed) {
+      if constexpr (kPacked) decode_keys<KB, DK, NT>(c, tid, src, src + kTile * (kRowK + kRowV), kdst);
+    } else {
+      copy_rows<KB, DK, NT>(c, true, kind, e0, ne, tid, kdst);
     }
-    if constexpr (PART != kKeys) {
-      live = ready(kVEmpty + st, ph);
-      if (!live) break;
-      if (it < packed) {
-        if constexpr (kPacked)
-          decode_values<VB, NT>(c, tid, src + kTile * kRowK, src + c.stage - value_meta_bytes(c.d), vdst);
-      } else {
-        copy_rows<VB, kTile, NT>(c, false, kind, e0, ne, tid, vdst);
-      }
-      arrive(kVFull + st);
+    arrive(kKFull + st);
+    live = ready(kVEmpty + st, ph);
+    if (!live) break;
+    if (it < packed) {
+      if constexpr (kPacked) decode_values<VB, NT>(c, tid, src + kTile * kRowK, src + kTile * (kRowK + kRowV) + kMetaBytes / 2, vdst);
+    } else {
+      copy_rows<VB, kTile, NT>(c, false, kind, e0, ne, tid, vdst);
     }
+    arrive(kVFull + st);
     if (kPacked && it < packed) {
       if (lane == 0) mbar_arrive(bars + 8 * (kRingEmpty + slot));
       if (++slot == c.stages) {

@@ -204,11 +204,11 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
   if (warp >= kSoftmaxThreads / 32) {
     const int pt = tid - kSoftmaxThreads;
     const Ctx c{d, cb, a, s, b, h, bh, __ffs(d.gk) - 1, __ffs(d.gv) - 1, __ffs(d.nvg) - 1,
-                base + Lay::kRing, base + Lay::kPages, stages, ring_stage_bytes(d)};
+                base + Lay::kRing, base + Lay::kPages, stages};
     with_bits(d, [&](auto kb, auto vb) {
       for (int i = 0; i < MT; ++i)
         copy_queries<kb.value, DK, kTile, kProducerThreads>(c, r0 + i * kTile, n_rows, pt, base + Lay::kQ + i * Lay::KH * kHalf);
-      produce<kb.value, vb.value, DK, kProducerThreads, kBoth, true>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
+      produce<kb.value, vb.value, DK, kProducerThreads, true>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
     });
   } else {
     const uint32_t ts = tmem + stream * kTile + lanes, to = tmem + 2 * kTile + stream * kTile + lanes;
@@ -427,7 +427,7 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
 template <int DK, int MT>
 cudaError_t launch(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s) {
   const int stages = ring_stages(d, Layout<DK, MT>::kFixed);
-  const int smem = Layout<DK, MT>::kFixed + stages * ring_stage_bytes(d);
+  const int smem = Layout<DK, MT>::kFixed + stages * ring_stage_bytes(d.kb, d.vb, d.dk);
   static SmemLimit limit;
   const cudaError_t e = limit.raise(chunk_wide_kernel<DK, MT>, smem);
   if (e != cudaSuccess) return e;
