@@ -1,4 +1,5 @@
-// Chunk attention with up to 16 query rows of a kv head (one or a few new tokens): the one-token
+// Chunk attention with up to 16 query rows of a kv head (one or a few new tokens), and with any number
+// over a cache with a side code, 16 at a time: the one-token
 // decode kernel's design (decode_mma.cuh) with a query row per MMA column.
 //
 // One CTA = 4 warps = one split of one (b, kv head): splits [0, splits_q) cover whole key groups of
@@ -34,7 +35,7 @@ using mma::kWarps;
 // Shared memory of one CTA: the queries for the zero-point MMA and scaled for the score MMA (each
 // u32 [NT][2*KSTEPS][32 lanes]), then barriers, copy counters, unit tags, failure flag, pages, and
 // the ring of stages.
-template <int KSTEPS, int NT>
+template <int KSTEPS, int NT, int SR>
 struct Smem {
   static constexpr int kQb = 0;
   static constexpr int kQf = kQb + NT * 2 * KSTEPS * 32 * 4;
@@ -43,16 +44,18 @@ struct Smem {
   static constexpr int kTag = kIssued + kMaxRing * 4;
   static constexpr int kFail = kTag + kMaxRing * 4;
   static constexpr int kPage = kFail + 16;
-  static constexpr int kStages = kBars + 256;
+  static constexpr int kQt = kPage + 16;                     // U_h^T q: fp32 [8 NT rows][SR]
+  static constexpr int kStages = kBars + (SR ? 256 + 8 * NT * SR * 4 : 256);
+  static_assert(kQt - kBars <= 256 && kStages % 128 == 0, "header");
 };
 
-template <int KB, int VB, int DK, int GV, int GK, int NT>
+template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int NT>
 struct Rings {
   // four CTAs an SM with one n-tile, two with two: their accumulators spill at 168 registers
   static constexpr int CTAS = NT == 1 ? 4 : 2;
   static constexpr int AVAIL = 233472 / CTAS - 1024;
-  static constexpr int HDR = Smem<DK / 16, NT>::kStages;
-  static constexpr int STAGE_Q = mma::quant_stage_bytes<KB, VB, DK, GV, GK, 0, 4>();
+  static constexpr int HDR = Smem<DK / 16, NT, SR>::kStages;
+  static constexpr int STAGE_Q = mma::quant_stage_bytes<KB, VB, DK, GV, GK, SR, SQ>();
   static constexpr int STAGE_F = mma::raw_stage_bytes<DK>();
   static constexpr int RING_Q = mma::ring_for(AVAIL - HDR, STAGE_Q, mma::kMinRing);
   static constexpr int RING_F = mma::ring_for(AVAIL - HDR, STAGE_F, kWarps);
@@ -61,18 +64,20 @@ struct Rings {
   static constexpr int BYTES = HDR + (STAGES > MERGE ? STAGES : MERGE);
 };
 
-template <int KB, int VB, int DK, int GV, int GK, int NT>
-__global__ void __launch_bounds__(kThreads, Rings<KB, VB, DK, GV, GK, NT>::CTAS)
+template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int NT>
+__global__ void __launch_bounds__(kThreads, Rings<KB, VB, DK, GV, GK, SR, SQ, NT>::CTAS)
 chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBufs cb,
                  const __grid_constant__ ChunkArgs a) {
   using G = mma::Quant<KB, VB, DK, GV>;
   using R = mma::Raw<DK>;
   constexpr int KSTEPS = DK / 16;
-  using RG = Rings<KB, VB, DK, GV, GK, NT>;
-  using SM = Smem<KSTEPS, NT>;
+  using RG = Rings<KB, VB, DK, GV, GK, SR, SQ, NT>;
+  using SM = Smem<KSTEPS, NT, SR>;
+  using Z = mma::Side<SR, SQ>;
   extern __shared__ __align__(128) unsigned char smem[];
 
-  const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x % a.splits, rb = blockIdx.x / a.splits * (8 * NT);   // the block's first query row
+  const int h = blockIdx.y, b = blockIdx.z;
   const int bh = b * d.Hkv + h;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qi = lane & 3;          // C columns 2qi, 2qi+1
@@ -107,7 +112,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   bool qok[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + qr;
+    const int r = rb + 8 * nt + qr;
     qok[nt] = r < n_rows && r % a.T < sw.n;
     qrow[nt] = a.q + (static_cast<size_t>(bh) * n_rows + (qok[nt] ? r : 0)) * DK;
   }
@@ -201,10 +206,41 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
             sm_qb[at] = ptx::h2_as_u32(pair);
           }
     }
+    float* sm_qt = reinterpret_cast<float*>(smem + SM::kQt);
+    if constexpr (SR > 0) {
+      // U_h^T q of every row: each lane sums DK/32 channels, then the warp reduces
+      const float* uh = cb.side_u + static_cast<size_t>(h) * DK * SR;
+      for (int r = warp; r < 8 * NT; r += kWarps) {
+        const bool ok = rb + r < n_rows && (rb + r) % a.T < sw.n;
+        const __half* qw = a.q + (static_cast<size_t>(bh) * n_rows + (ok ? rb + r : 0)) * DK;
+        float acc[SR];
+#pragma unroll
+        for (int i = 0; i < SR; ++i) acc[i] = 0.0f;
+#pragma unroll
+        for (int cc = 0; cc < DK / 32; ++cc) {
+          const int ch = lane + 32 * cc;
+          const float qc = ok ? __half2float(qw[ch]) : 0.0f;
+#pragma unroll
+          for (int i4 = 0; i4 < SR; i4 += 4) {
+            const float4 u4 = *reinterpret_cast<const float4*>(uh + ch * SR + i4);
+            acc[i4] = fmaf(u4.x, qc, acc[i4]);
+            acc[i4 + 1] = fmaf(u4.y, qc, acc[i4 + 1]);
+            acc[i4 + 2] = fmaf(u4.z, qc, acc[i4 + 2]);
+            acc[i4 + 3] = fmaf(u4.w, qc, acc[i4 + 3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < SR; ++i) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+          if (lane == 0) sm_qt[r * SR + i] = acc[i];
+        }
+      }
+    }
     __syncthreads();
     // retained positions, one per lane (ascending), for masking the quantized tiles
     const int ret_pos = lane < sw.n_ret ? retained_position(sw.Q, lane) : -1;
-    const mma::StageLayout L = mma::quant_stage_layout(GK, DK, KB, VB, G::NVG);
+    const mma::StageLayout L = mma::quant_stage_layout(GK, DK, KB, VB, G::NVG, Z::ZB, SR);
     constexpr int MT = GK / 16;
     const bool swap = qi >= 2;
     const uint32_t sel_lo = swap ? 0x1054u : 0x5410u;
@@ -240,6 +276,10 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
       ptx::bulk_g2s(dst + L.kmeta_off, cb.ksz + gi * DK, DK * 4, bar);
       ptx::bulk_g2s(dst + L.v_off, cb.vcode + tok * G::VW, GK * G::VBYTES_ROW, bar);
       ptx::bulk_g2s(dst + L.vmeta_off, cb.vsz + tok * G::NVG, GK * G::NVG * 4, bar);
+      if constexpr (SR > 0) {
+        ptx::bulk_g2s(dst + L.z_off, cb.zcode + tok * Z::ZB, GK * Z::ZB, bar);
+        ptx::bulk_g2s(dst + L.zmeta_off, cb.zsz + gi * SR, SR * 4, bar);
+      }
     };
     if (threadIdx.x == 0)
       for (int k = 0; k < RING && k < n_units; ++k) issue(k, group_of(k, false));
@@ -306,6 +346,28 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
         }
       }
 
+      // the side code: its scales into U_h^T q, its zeros into the bias
+      uint32_t bz[NT];
+      if constexpr (SR > 0) {
+        const __half2* zm = reinterpret_cast<const __half2*>(S + L.zmeta_off);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          bz[nt] = 0u;
+          if (qi < Z::NQ) {
+            const float f = 1.0f / static_cast<float>(1 << Z::pos(qi));
+            const float* qt = sm_qt + (8 * nt + qr) * SR;
+            bz[nt] = ptx::h2_as_u32(__floats2half2_rn(qt[qi] * __low2float(zm[qi]) * f,
+                                                      qt[qi + Z::NQ] * __low2float(zm[qi + Z::NQ]) * f));
+          }
+#pragma unroll
+          for (int i = 0; i < SR; ++i) {
+            const float zero = __high2float(zm[i]);
+            cbias[nt][0] = fmaf(sm_qt[(8 * nt + 2 * qi) * SR + i], zero, cbias[nt][0]);
+            cbias[nt][1] = fmaf(sm_qt[(8 * nt + 2 * qi + 1) * SR + i], zero, cbias[nt][1]);
+          }
+        }
+      }
+
       // ---- scores of the whole group: tokens 16 mt + qr, + 8; rows 2qi, 2qi + 1 of every n-tile ----
       float sc[NT][MT][4];
 #pragma unroll
@@ -331,6 +393,21 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
             for (int nt = 0; nt < NT; ++nt)
               ptx::mma_16816(cs[nt], r0[2 * ls], r1[2 * ls], r0[2 * ls + 1], r1[2 * ls + 1], bq[nt][s][0], bq[nt][s][1]);
           }
+        }
+        if constexpr (SR > 0) {
+          const unsigned char* zr = S + L.z_off;
+          uint32_t x0, x1;
+          if constexpr (Z::ZB == 4) {
+            x0 = *reinterpret_cast<const uint32_t*>(zr + t0 * 4);
+            x1 = *reinterpret_cast<const uint32_t*>(zr + (t0 + 8) * 4);
+          } else {
+            // (c0 c1 | c2 c3) of a 16-bit row -> c0 c1 in the low half, c2 c3 in the high half
+            x0 = ptx::prmt(*reinterpret_cast<const uint16_t*>(zr + t0 * 2), 0u, 0x0100u);
+            x1 = ptx::prmt(*reinterpret_cast<const uint16_t*>(zr + (t0 + 8) * 2), 0u, 0x0100u);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            ptx::mma_1688(cs[nt], (x0 >> Z::shift(qi)) & Z::mask(qi), (x1 >> Z::shift(qi)) & Z::mask(qi), bz[nt]);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -553,7 +630,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          cs[nt][e] = sees(e0 + qr + 8 * (e >> 1), 8 * nt + 2 * qi + (e & 1)) ? cs[nt][e] * alpha : -INFINITY;
+          cs[nt][e] = sees(e0 + qr + 8 * (e >> 1), rb + 8 * nt + 2 * qi + (e & 1)) ? cs[nt][e] * alpha : -INFINITY;
         rescale(nt, fmaxf(cs[nt][0], cs[nt][2]), fmaxf(cs[nt][1], cs[nt][3]));
         float p[4];
 #pragma unroll
@@ -646,9 +723,9 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
       }
     }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < min(NR, n_rows) * kDV; idx += kThreads) {
+  for (int idx = threadIdx.x; idx < min(NR, n_rows - rb) * kDV; idx += kThreads) {
     const int r = idx / kDV, c = idx % kDV;
-    if (r % a.T >= sw.n) continue;
+    if ((rb + r) % a.T >= sw.n) continue;
     float M = -INFINITY;
 #pragma unroll
     for (int ww = 0; ww < kWarps; ++ww) M = fmaxf(M, sm_ml[(ww * NR + r) * 2]);
@@ -660,7 +737,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
       acc = fmaf(wt, sm_o[(ww * NR + r) * kDV + c], acc);
       lsum = fmaf(wt, sm_ml[(ww * NR + r) * 2 + 1], lsum);
     }
-    const long long row = static_cast<long long>(bh) * n_rows + r, pi = row * a.splits + split;
+    const long long row = static_cast<long long>(bh) * n_rows + rb + r, pi = row * a.splits + split;
     if (!KVQ_IN_BOUNDS(d, kSiteChunkPartial, row, static_cast<long long>(d.B) * d.Hq * a.T)) continue;
     if (a.splits == 1) {
       a.out[row * kDV + c] = __float2half_rn(lsum > 0.0f ? acc / lsum : 0.0f);
@@ -671,30 +748,39 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   }
 }
 
-template <int KB, int VB, int DK, int GV, int GK, int NT>
+template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int NT>
 cudaError_t launch(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s) {
-  using RG = Rings<KB, VB, DK, GV, GK, NT>;
+  using RG = Rings<KB, VB, DK, GV, GK, SR, SQ, NT>;
   static SmemLimit limit;
-  const cudaError_t e = limit.raise(chunk_few_kernel<KB, VB, DK, GV, GK, NT>, RG::BYTES);
+  const cudaError_t e = limit.raise(chunk_few_kernel<KB, VB, DK, GV, GK, SR, SQ, NT>, RG::BYTES);
   if (e != cudaSuccess) return e;
-  chunk_few_kernel<KB, VB, DK, GV, GK, NT><<<dim3(a.splits, d.Hkv, d.B), kThreads, RG::BYTES, s>>>(d, c, a);
+  const int blocks = (d.n_rep * a.T + 8 * NT - 1) / (8 * NT);
+  chunk_few_kernel<KB, VB, DK, GV, GK, SR, SQ, NT><<<dim3(a.splits * blocks, d.Hkv, d.B), kThreads, RG::BYTES, s>>>(d, c, a);
   return cudaGetLastError();
 }
 
-// The built instances, F(KB, VB, DK, GV, GK): the decode kernel's bit widths and group sizes.
-#define KVQ_CHUNK_FEW_4(F) \
-  F(4, 2, 128, 64, 64) F(4, 2, 128, 32, 32) F(4, 2, 32, 32, 32) F(4, 2, 32, 64, 64) F(4, 4, 128, 64, 64) F(4, 4, 32, 64, 64)
-#define KVQ_CHUNK_FEW_28(F) \
-  F(8, 4, 128, 64, 64) F(8, 4, 128, 32, 32) F(8, 4, 32, 64, 64) F(2, 2, 128, 64, 64) F(2, 2, 128, 32, 32)
+// The built instances, F(KB, VB, DK, GV, GK, SR, SQ): the decode kernel's bit widths, group sizes and
+// side codes.
+#define KVQ_CHUNK_FEW_4(F)                                                                     \
+  F(4, 2, 128, 64, 64, 0, 4) F(4, 2, 128, 32, 32, 0, 4) F(4, 2, 32, 32, 32, 0, 4)              \
+  F(4, 2, 32, 64, 64, 0, 4) F(4, 4, 128, 64, 64, 0, 4) F(4, 4, 32, 64, 64, 0, 4)
+#define KVQ_CHUNK_FEW_28(F)                                                                    \
+  F(8, 4, 128, 64, 64, 0, 4) F(8, 4, 128, 32, 32, 0, 4) F(8, 4, 32, 64, 64, 0, 4)              \
+  F(2, 2, 128, 64, 64, 0, 4) F(2, 2, 128, 32, 32, 0, 4)
+#define KVQ_CHUNK_FEW_SIDE(F)                                                                  \
+  F(4, 2, 128, 64, 64, 4, 4) F(4, 2, 128, 64, 64, 4, 8) F(4, 2, 128, 64, 64, 8, 4)             \
+  F(2, 2, 128, 64, 64, 4, 4) F(2, 2, 128, 64, 64, 4, 8) F(2, 2, 128, 64, 64, 8, 4)
 
 using LaunchFn = cudaError_t (*)(const Dims&, const CacheBufs&, const ChunkArgs&, cudaStream_t);
 // The instance for a cache and number of rows, or null (each file knows its own).
 LaunchFn find_4(const Dims& d, int rows);
 LaunchFn find_28(const Dims& d, int rows);
+LaunchFn find_side(const Dims& d, int rows);
 
-#define KVQ_CHUNK_FEW_ENTRY(KB, VB, DK, GV, GK)                                        \
-  if (d.kb == KB && d.vb == VB && d.dk == DK && d.gv == GV && d.gk == GK)              \
-    return rows <= 8 ? &launch<KB, VB, DK, GV, GK, 1> : &launch<KB, VB, DK, GV, GK, 2>;
+#define KVQ_CHUNK_FEW_ENTRY(KB, VB, DK, GV, GK, SR, SQ)                                        \
+  if (d.kb == KB && d.vb == VB && d.dk == DK && d.gv == GV && d.gk == GK && d.sr == SR &&      \
+      (SR == 0 || d.sq == SQ))                                                                 \
+    return rows <= 8 ? &launch<KB, VB, DK, GV, GK, SR, SQ, 1> : &launch<KB, VB, DK, GV, GK, SR, SQ, 2>;
 
 }  // namespace few
 }  // namespace kvq

@@ -11,14 +11,21 @@ LaunchFn find_4(const Dims& d, int rows) {
 
 }  // namespace few
 
-bool chunk_few_supported(const Dims& d, int T) {
-  if (d.var || d.sr || d.dv != few::kDV || d.n_rep * T > 16) return false;
-  return few::find_4(d, d.n_rep * T) || few::find_28(d, d.n_rep * T);
+namespace {
+few::LaunchFn find(const Dims& d, int T) {
+  const int rows = d.n_rep * T;
+  if (d.var || d.dv != few::kDV) return nullptr;
+  if (d.sr) return few::find_side(d, rows);
+  if (rows > 16) return nullptr;
+  few::LaunchFn fn = few::find_4(d, rows);
+  return fn ? fn : few::find_28(d, rows);
 }
+}  // namespace
+
+bool chunk_few_supported(const Dims& d, int T) { return find(d, T) != nullptr; }
 
 cudaError_t launch_chunk_few(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s) {
-  few::LaunchFn fn = few::find_4(d, d.n_rep * a.T);
-  if (!fn) fn = few::find_28(d, d.n_rep * a.T);
+  few::LaunchFn fn = find(d, a.T);
   return fn ? fn(d, c, a, s) : cudaErrorNotSupported;
 }
 

@@ -125,7 +125,7 @@ struct ChunkArgs {
 int chunk_simple_splits(const Dims& d, int L, int T, int num_splits);
 int chunk_mma_splits(const Dims& d, int L, int T, int num_splits);
 bool chunk_mma_supported(const Dims& d);
-// One or a few new tokens, up to 16 query rows of a kv head (chunk_few.cuh).
+// One or a few new tokens, up to 16 query rows of a kv head, or a cache with a side code (chunk_few.cuh).
 bool chunk_few_supported(const Dims& d, int T);
 cudaError_t launch_chunk_few(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s);
 // Up to this many query rows of a kv head the tokens take the MMA's rows (chunk_narrow.cu); with 64

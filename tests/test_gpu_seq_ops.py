@@ -96,7 +96,11 @@ def reference(tw, b, q, k_new, v_new, sees):
     output: the output's own rounding u |o|; a weight and a value rounded to fp16 once each,
     2 u sum_j p_j |v_j|; keys (and the query side of a side code) rounded to fp16 once, which
     moves score j by at most d_j = u sum_c |q_c k_jc| / sqrt(d_k) and so the output by
-    sum_j p_j d_j |v_j - o| to first order.  The factor 1.05 covers the second order and the
+    sum_j p_j d_j |v_j - o| to first order.  The kernel for few rows rounds the products q_c s_c
+    of query and key scale instead: an error u |q_c s_c code| with s_c code = k_jc - z_c, z_c being
+    the group's smallest key, so |k_jc| + max |k_.c| over the group takes the place of |k_jc|; and
+    the weights' products with the value scale instead of weight and value, where likewise
+    |s code| <= |v_j| + |z_j|, z_j the smallest value of the token's group.  The factor 1.05 covers the second order and the
     fp32 sums (relative 2^-24 a step over at most a few thousand steps)."""
     cfg = tw.cfg
     oc = tw.oc[b]
@@ -111,17 +115,23 @@ def reference(tw, b, q, k_new, v_new, sees):
         kk, vv = k_new[h].astype(np.float64), v_new[h].astype(np.float64)
         L = 0
         zh = None
+        ka, va = np.abs(kk), np.abs(vv)
         if oc is not None:
             kh, vh = oc.decoded_kv(0, h)
             L = kh.shape[0]
             kk, vv = np.concatenate([kh, kk]), np.concatenate([vh, vv])
+            Q, gk, gv = oc.Q, cfg["group_k"], cfg["group_v"]
+            ka, va = np.abs(kk), np.abs(vv)
+            if Q:
+                ka[:Q] += np.repeat(np.abs(kh[:Q]).reshape(Q // gk, gk, -1).max(1), gk, axis=0)
+                va[:Q] += np.repeat(np.abs(vh[:Q]).reshape(Q, -1, gv).max(2), gv, axis=1)
             if cfg.get("side_rank"):
                 zh = oc.decoded_side(0, h)
         for r in range(n_rep):
             hq = h * n_rep + r
             qq = q[hq].astype(np.float64)
             s = qq @ kk.T
-            mag = np.abs(qq) @ np.abs(kk).T
+            mag = np.abs(qq) @ ka.T
             if zh is not None:
                 qt = np.stack([O.side_query(oc.U[h], x) for x in qq])
                 s[:, :L] += qt @ zh.T
@@ -135,7 +145,7 @@ def reference(tw, b, q, k_new, v_new, sees):
             out[hq] = o
             delta = U16 * mag / math.sqrt(dk)
             spread = np.einsum("tj,tjc->tc", p * delta, np.abs(vv[None] - o[:, None]))
-            bound[hq] = 1.05 * (U16 * np.abs(o) + 2 * U16 * (p @ np.abs(vv)) + spread) + 2.0 ** -25
+            bound[hq] = 1.05 * (U16 * np.abs(o) + 2 * U16 * (p @ va) + spread) + 2.0 ** -25
     return out, bound
 
 
@@ -217,8 +227,9 @@ def test_chunk_group_sizes_and_windows(gk, gv, R, ret):
 @pytest.mark.parametrize("extra", [
     dict(side_rank=4, side_bits=4), dict(side_rank=8, side_bits=4, rot_keys=1), dict(rot_keys=1), dict(paged=1),
     dict(paged=1, side_rank=4, side_bits=8, k_bits=2), VAR, dict(VAR, paged=1)])
-def test_chunk_cache_forms(extra):
-    check_chunk(Twin(config(**extra), [640, 300, 127], seed=11), 5, splits=(0, 2))
+@pytest.mark.parametrize("T", [1, 5, 17])
+def test_chunk_cache_forms(extra, T):
+    check_chunk(Twin(config(**extra), [640, 300, 127], seed=11), T, splits=(0, 2))
 
 
 @pytest.mark.parametrize("T,counts", [(5, [5, 0, 2]), (40, [1, 40, 33]), (3, [0, 0, 0])])
