@@ -247,14 +247,17 @@ int kvq_free_pages(const kvq_cache* cache);
  * are not in the cache and this call does not put them there (kvq_append_tokens does).
  * q fp16 [B][Hq][T][d_k], k_new fp16 [B][Hkv][T][d_k], v_new fp16 [B][Hkv][T][d_v], T >= 1:
  * sequence b's first counts[b] tokens are valid (counts: host int[B], each in [0, T]; NULL: T
- * each); rows behind them are neither read nor, in out fp16 [B][Hq][T][d_v], written.  Token t
+ * each); the contents of the rows behind them do not matter, and in out fp16 [B][Hq][T][d_v]
+ * they are not written.  Token t
  * of a sequence attends over all of the sequence's cached tokens and over the new tokens it
  * sees: tokens 0 .. t, or, with mask (device u32 [B][T][ceil(T/32)]), the tokens j with bit
  * j % 32 of word j / 32 of its row set, in any pattern (those behind counts[b] never).  A
  * sequence may be empty; a row that sees nothing at all gives zeros.  Scores, side codes and
  * rotation as for kvq_decode_attention, the new tokens counting as fp16 tokens.
- * The tensor-core path rounds each decoded key and value and each softmax weight to fp16 once;
- * sums, maxima and accumulators are fp32.
+ * The tensor-core paths round each decoded key and value and each softmax weight to fp16 once, or
+ * (few query rows) the products q_c * scale_c of query and key scale, which like those of the
+ * decode must stay within fp16, and of weight and value scale; sums, maxima and accumulators are
+ * fp32.
  * workspace: device scratch of kvq_chunk_workspace_size bytes (0: may be NULL), for the cache's
  * current lengths, T and num_splits (0 = automatic, else splits of the tokens of each row,
  * clamped).  status: device u32 the kernel ORs KVQ_STATUS_* bits into, never cleared here; the

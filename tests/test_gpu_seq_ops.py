@@ -203,14 +203,18 @@ def test_chunk_over_short_and_empty_caches(lengths):
     check_chunk(Twin(config(), lengths, seed=sum(lengths)), 4, splits=(0, 1))
 
 
-@pytest.mark.parametrize("kb,vb", [(8, 4), (2, 2), (4, 4), (8, 8), (2, 4), (16, 16)])
-def test_chunk_bit_widths(kb, vb):
-    check_chunk(Twin(config(k_bits=kb, v_bits=vb), [600, 601, 333], seed=kb * 10 + vb), 6)
+@pytest.mark.parametrize("kb,vb", [(8, 4), (2, 2), (4, 4), (8, 8), (2, 4), (4, 8), (16, 16)])
+@pytest.mark.parametrize("T", [2, 3, 6, 20, 40])       # 8, 12, 24, 80 and 160 query rows of a kv head
+def test_chunk_bit_widths(kb, vb, T):
+    check_chunk(Twin(config(k_bits=kb, v_bits=vb), [600, 601, 333], seed=kb * 10 + vb), T,
+                kernels=KERNELS if T == 6 else KERNELS[:1])
 
 
-@pytest.mark.parametrize("dk,dv", [(32, 128), (64, 128), (128, 64), (256, 256), (32, 32)])
-def test_chunk_head_dims(dk, dv):
-    check_chunk(Twin(config(d_k=dk, d_v=dv, group_v=32), [400, 257, 90], seed=dk + dv), 5)
+@pytest.mark.parametrize("dk,dv,kb", [(32, 128, 4), (64, 128, 4), (128, 64, 4), (256, 256, 4), (32, 32, 4), (32, 128, 2),
+                                      (64, 128, 2), (32, 128, 8), (64, 128, 8)])
+@pytest.mark.parametrize("T", [3, 5, 45])
+def test_chunk_head_dims(dk, dv, kb, T):
+    check_chunk(Twin(config(d_k=dk, d_v=dv, k_bits=kb, group_v=32, group_k=32), [400, 257, 90], seed=dk + dv), T)
 
 
 @pytest.mark.parametrize("n_q,n_kv", [(2, 2), (4, 2), (16, 2), (3, 1)])
@@ -220,14 +224,15 @@ def test_chunk_query_groups(n_q, n_kv):
 
 @pytest.mark.parametrize("gk,gv,R,ret", [(16, 16, 0, 1), (32, 32, 64, 0), (128, 128, 5, 1), (64, 32, 300, 1),
                                          (32, 64, 1, 0)])
-def test_chunk_group_sizes_and_windows(gk, gv, R, ret):
-    check_chunk(Twin(config(group_k=gk, group_v=gv, window=R, log_retain=ret), [777, 130, 33], seed=gk), 3)
+@pytest.mark.parametrize("T", [3, 8, 40])
+def test_chunk_group_sizes_and_windows(gk, gv, R, ret, T):
+    check_chunk(Twin(config(group_k=gk, group_v=gv, window=R, log_retain=ret), [777, 130, 33], seed=gk), T)
 
 
 @pytest.mark.parametrize("extra", [
     dict(side_rank=4, side_bits=4), dict(side_rank=8, side_bits=4, rot_keys=1), dict(rot_keys=1), dict(paged=1),
     dict(paged=1, side_rank=4, side_bits=8, k_bits=2), VAR, dict(VAR, paged=1)])
-@pytest.mark.parametrize("T", [1, 5, 17])
+@pytest.mark.parametrize("T", [1, 4, 7, 17, 45])
 def test_chunk_cache_forms(extra, T):
     check_chunk(Twin(config(**extra), [640, 300, 127], seed=11), T, splits=(0, 2))
 
@@ -275,6 +280,52 @@ def test_chunk_of_one_is_the_next_decode():
     b = tw.gc.decode(q[:, :, 0].contiguous()).float()
     # two fp32 computations rounded to fp16 each: a step of the larger, plus fp32 noise
     assert torch.all((a - b).abs() <= 2 * U16 * torch.maximum(a.abs(), b.abs()) + 1e-5)
+
+
+def test_chunk_and_append_far_into_a_large_cache():
+    """Element offsets beyond 2^31: the last heads of an fp16 cache of 2.2 million slots."""
+    need_gpu()
+    tw = Twin(config(batch=1, n_q_heads=16, n_kv_heads=8, k_bits=16, v_bits=16, max_context=2200000), [0])
+    k, v = tw.tokens(300)
+    tw.gc.prefill_sequence(0, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda())
+    small = O.OracleCache(dict(tw.cfg, max_context=400))
+    small.prefill(k[None], v[None])
+    tw.oc[0] = small
+    for T in (2, 40, 80):
+        check_chunk(tw, T, kernels=KERNELS[:1])
+    _, kn, vn = tw.chunk(5)
+    tw.gc.append_tokens(torch.from_numpy(kn).cuda(), torch.from_numpy(vn).cuda())
+    tw.append_oracle(0, kn[0], vn[0])
+    assert np.array_equal(tw.gc.view("win_k")[0, :, :305].cpu().numpy(), small.win_k[0, :, :305])
+    assert np.array_equal(tw.gc.view("win_v")[0, :, :305].cpu().numpy(), small.win_v[0, :, :305])
+
+
+def test_chunk_calls_on_two_streams_do_not_meet():
+    """Two calls on one cache at once: each has its own workspace."""
+    tw = Twin(config(), [900, 700, 800], seed=14)
+    qa = [torch.from_numpy(x).cuda() for x in tw.chunk(3)]
+    qb = [torch.from_numpy(x).cuda() for x in tw.chunk(30)]
+    wa, wb = tw.gc.chunk_attention(*qa), tw.gc.chunk_attention(*qb)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(8):
+        outs.append((tw.gc.chunk_attention(*qa, stream=s1), tw.gc.chunk_attention(*qb, stream=s2)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, wa) and torch.equal(b, wb) for a, b in outs)
+
+
+def test_chunk_large_values_and_keys():
+    """Values up to a thousand and keys up to a hundred: no product of a weight and a scale leaves fp16."""
+    tw = Twin(config(v_bits=2), [0, 0, 0], seed=15)
+    for b, L in enumerate((400, 300, 200)):
+        k, v = tw.tokens(L)
+        k, v = (k * 10).astype(np.float16), (v * 300).astype(np.float16)
+        tw.gc.prefill_sequence(b, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda())
+        tw.oc[b] = tw.oracle()
+        tw.oc[b].prefill(k[None], v[None])
+    for T in (1, 4, 8, 20, 40):
+        check_chunk(tw, T, kernels=KERNELS[:1])
 
 
 def test_chunk_refusals():
