@@ -259,7 +259,7 @@ int kvq_free_pages(const kvq_cache* cache);
  * decode must stay within fp16, and of weight and value scale; sums, maxima and accumulators are
  * fp32.
  * workspace: device scratch of kvq_chunk_workspace_size bytes (0: may be NULL), for the cache's
- * current lengths, T and num_splits (0 = automatic, else splits of the tokens of each row,
+ * current lengths and kernel selection, T and num_splits (0 = automatic, else splits of the tokens of each row,
  * clamped).  status: device u32 the kernel ORs KVQ_STATUS_* bits into, never cleared here; the
  * first word of a decode workspace serves.  T * n_q_heads < 2^24 and B * T * n_q_heads < 2^31
  * (UNSUPPORTED otherwise); counts or lengths that differ need B <= KVQ_MAX_SEQS.
@@ -328,7 +328,9 @@ int kvq_decode_attention(kvq_cache* cache, const void* q, void* out, void* works
 
 /* Decode kernel selection for a cache (default KVQ_KERNEL_AUTO: the tensor-core
  * kernel where it is built for the shape, else the generic CUDA-core kernel).
- * KVQ_KERNEL_TENSOR fails with UNSUPPORTED on shapes it is not built for. */
+ * KVQ_KERNEL_TENSOR fails with UNSUPPORTED on shapes it is not built for.  kvq_chunk_attention
+ * follows it too: over per-channel widths KVQ_KERNEL_AUTO leaves short caches to the generic
+ * kernel, KVQ_KERNEL_TENSOR does not. */
 #define KVQ_KERNEL_AUTO     0
 #define KVQ_KERNEL_GENERIC  1
 #define KVQ_KERNEL_TENSOR   2

@@ -83,7 +83,7 @@ chunk_simple_kernel(Dims d, CacheBufs cb, const __grid_constant__ ChunkArgs a) {
   }
   // tokens: the quantized prefix, the fp16 list (retained, window), the new ones
   const int n_old = sw.Q + sw.n_ret + (sw.L - sw.Q), n_all = n_old + sw.n;
-  const int begin = static_cast<int>(static_cast<long long>(split) * n_all / a.splits);
+  const int begin = a.new_only ? n_old : static_cast<int>(static_cast<long long>(split) * n_all / a.splits);
   const int end = static_cast<int>(static_cast<long long>(split + 1) * n_all / a.splits);
   const int mask_words = (a.T + 31) / 32;
 
@@ -216,11 +216,12 @@ chunk_simple_kernel(Dims d, CacheBufs cb, const __grid_constant__ ChunkArgs a) {
       Lsum = fmaf(wk[k], sm_l[k][r], Lsum);
     }
     const size_t part = row * a.splits + split;
-    if (a.splits > 1 && threadIdx.x == 0) a.ml[part] = make_float2(M, Lsum);
+    const bool partial = a.splits > 1 || a.new_only;
+    if (partial && threadIdx.x == 0) a.ml[part] = make_float2(M, Lsum);
     for (int ch = threadIdx.x; ch < d.dv; ch += blockDim.x) {
       float acc = 0.0f;
       for (int k = 0; k < kWarps; ++k) acc = fmaf(wk[k], sm_o[k][r][ch], acc);
-      if (a.splits > 1)
+      if (partial)
         a.o[part * d.dv + ch] = acc;
       else
         a.out[row * d.dv + ch] = __float2half_rn(Lsum > 0.0f ? acc / Lsum : 0.0f);   // a row that sees nothing: 0
@@ -280,6 +281,50 @@ chunk_combine_kernel(Dims d, const __grid_constant__ ChunkArgs a, long long rows
   }
 }
 
+// q [B * Hq][T][dk] to [T][B * Hq][dk], 16 bytes a thread.
+__global__ void __launch_bounds__(256)
+step_queries_kernel(const uint4* __restrict__ q, uint4* __restrict__ steps, int rows, int T, int vec) {
+  const long long n = static_cast<long long>(rows) * T * vec;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+    const int e = static_cast<int>(i % vec), t = static_cast<int>(i / vec % T);
+    steps[(static_cast<long long>(t) * rows + i / vec / T) * vec + e] = q[i];
+  }
+}
+
+// Merge of a row's decode-step partials (of tokens t0 to t0 + nt - 1) with that of its new tokens,
+// a warp per row.
+__global__ void __launch_bounds__(128)
+combine_steps_kernel(Dims d, const __grid_constant__ ChunkArgs a, const float2* __restrict__ step_ml,
+                     const float* __restrict__ step_o, int step_splits, int t0, int nt) {
+  const int lane = threadIdx.x & 31;
+  const int heads = d.B * d.Hq;
+  const int i = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5);   // (token, sequence, head)
+  if (i >= nt * heads) return;
+  const int t = t0 + i / heads, bh = i % heads;
+  if (t >= a.seq.n[a.seq.uniform ? 0 : bh / d.Hq]) return;
+  const long long row = static_cast<long long>(bh) * a.T + t;
+  const long long first = static_cast<long long>(i) * step_splits;
+  float M = a.ml[row].x;
+  for (int s = lane; s < step_splits; s += 32) M = fmaxf(M, step_ml[first + s].x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float den = 0.0f, num[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = 0; s <= step_splits; ++s) {
+    const float2 v = s < step_splits ? step_ml[first + s] : a.ml[row];
+    const float* o = s < step_splits ? step_o + (first + s) * d.dv : a.o + row * d.dv;
+    const float w = v.x == -INFINITY ? 0.0f : exp2f(v.x - M);
+    den = fmaf(w, v.y, den);
+    if (w == 0.0f) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < d.dv) num[i] = fmaf(w, o[lane + 32 * i], num[i]);
+  }
+  const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (lane + 32 * i < d.dv) a.out[row * d.dv + lane + 32 * i] = __float2half_rn(num[i] * inv);
+}
+
 __global__ void __launch_bounds__(256)
 rotate_rows_kernel(Dims d, const __half* __restrict__ src, __half* __restrict__ dst, long long rows, float inv_c) {
   const int lane = threadIdx.x & 31;
@@ -323,6 +368,22 @@ cudaError_t launch_chunk_combine(const Dims& d, const ChunkArgs& a, cudaStream_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, chunk_combine_kernel, d, a, rows);
+}
+
+cudaError_t launch_step_queries(const Dims& d, const __half* q, __half* steps, int T, cudaStream_t s) {
+  const long long n = static_cast<long long>(d.B) * d.Hq * T * (d.dk / 8);
+  const unsigned ctas = static_cast<unsigned>(std::min<long long>((n + 255) / 256, 148 * 16));
+  step_queries_kernel<<<ctas, 256, 0, s>>>(reinterpret_cast<const uint4*>(q), reinterpret_cast<uint4*>(steps),
+                                           d.B * d.Hq, T, d.dk / 8);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_steps(const Dims& d, const ChunkArgs& a, const float2* step_ml, const float* step_o,
+                                 int step_splits, int t0, cudaStream_t s) {
+  const int nt = std::min(kStepTokens, a.T - t0);
+  const long long rows = static_cast<long long>(d.B) * d.Hq * nt;
+  combine_steps_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(d, a, step_ml, step_o, step_splits, t0, nt);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_rotate_rows(const Dims& d, const __half* src, __half* dst, long long rows, float inv_c,

@@ -1087,9 +1087,10 @@ int check_counts(const kvq_cache* c, int T, const int* counts) {
 
 // How a chunk attention runs: its split count and its workspace.
 struct ChunkPlan {
-  enum { kSimple, kTile, kFew } kernel;
+  enum { kSimple, kTile, kFew, kSteps } kernel;
   int splits, splits_q;                 // partials per row; of those over the quantized groups (kFew)
-  size_t ml, o, rot_q, rot_k, bytes;   // offsets of the workspace's parts, and its size
+  kvq_plan steps;                       // kSteps: of one decode step (its splits: steps.splits_quant + _fp16)
+  size_t ml, o, rot_q, rot_k, step_q, step_ml, step_o, bytes;   // offsets of the workspace's parts, its size
 };
 
 int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
@@ -1099,10 +1100,21 @@ int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
   if (rows >= (1LL << 31) || static_cast<long long>(d.Hq) * T >= (1LL << 24)) return KVQ_ERR_UNSUPPORTED;
   int longest = 0;
   for (int b = 0; b < d.B; ++b) longest = std::max(longest, c->L[b]);
+  // A width map's chunk as decode steps costs 10 to 17 us a token of launches and prologues on short
+  // caches, the CUDA-core kernel about 0.5 ns a (query head, cached token) and new token: 8 new
+  // tokens over 1 x 32 heads x 1024 tokens 185 and 166 us, x 4096 tokens 191 and 476 us, over
+  // 8 x 32 x 64 tokens 137 and 71 us, x 256 tokens 141 and 262 us; 8 x 32 x 32k 0.74 and 29 ms.
+  const bool steps = d.var && kvq::decode_var_supported(d) &&
+                     (c->kernel == KVQ_KERNEL_TENSOR ||
+                      static_cast<long long>(d.B) * d.Hq * longest > 32768);
   p->kernel = ChunkPlan::kSimple;
   if (c->kernel != KVQ_KERNEL_GENERIC)
-    p->kernel = kvq::chunk_few_supported(d, T) ? ChunkPlan::kFew : kvq::chunk_mma_supported(d) ? ChunkPlan::kTile : ChunkPlan::kSimple;
+    p->kernel = kvq::chunk_few_supported(d, T) ? ChunkPlan::kFew
+                : kvq::chunk_mma_supported(d)  ? ChunkPlan::kTile
+                : steps                        ? ChunkPlan::kSteps
+                                               : ChunkPlan::kSimple;
   p->splits_q = 0;
+  p->steps.splits_quant = p->steps.splits_fp16 = 0;
   if (p->kernel == ChunkPlan::kFew) {
     // the decode planner's split counts, the new tokens behind the fp16 list
     int nG = 0, nF = 0;
@@ -1117,6 +1129,10 @@ int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
     if (rc) return rc;
     p->splits_q = plan.splits_quant;
     p->splits = plan.splits_quant + plan.splits_fp16;
+  } else if (p->kernel == ChunkPlan::kSteps) {
+    p->splits = 1;
+    const int rc = plan_cache(c, num_splits, true, &p->steps);
+    if (rc) return rc;
   } else {
     p->splits = (p->kernel == ChunkPlan::kTile ? kvq::chunk_mma_splits : kvq::chunk_simple_splits)(d, longest, T, num_splits);
   }
@@ -1127,13 +1143,61 @@ int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
     at += up(bytes);
     return here;
   };
-  const bool partials = p->splits > 1;
+  const bool partials = p->splits > 1 || p->kernel == ChunkPlan::kSteps;
+  const size_t step_rows = static_cast<size_t>(d.B) * d.Hq * std::min(T, kvq::kStepTokens) * (p->steps.splits_quant + p->steps.splits_fp16);
   p->ml = take(partials ? rows * p->splits * sizeof(float2) : 0);
   p->o = take(partials ? rows * p->splits * d.dv * sizeof(float) : 0);
   p->rot_q = take(d.rot ? rows * d.dk * 2 : 0);
   p->rot_k = take(d.rot ? static_cast<size_t>(d.B) * d.Hkv * T * d.dk * 2 : 0);
+  p->step_q = take(p->kernel == ChunkPlan::kSteps && T > 1 ? rows * d.dk * 2 : 0);
+  p->step_ml = take(step_rows * sizeof(float2));
+  p->step_o = take(step_rows * d.dv * sizeof(float));
   p->bytes = at;
   return KVQ_OK;
+}
+
+// A width map's chunk: the one-token decode kernel for every new token's queries over the cached
+// tokens, the new tokens on CUDA cores, one merge.
+int run_steps(const kvq_cache* c, const ChunkPlan& p, kvq::ChunkArgs& a, char* ws, cudaStream_t s) {
+  const kvq::Dims& d = c->d;
+  const kvq::CacheBufs cb = cache_bufs(c);
+  float2* ml = reinterpret_cast<float2*>(ws + p.step_ml);
+  float* o = reinterpret_cast<float*>(ws + p.step_o);
+  const __half* q = a.q;                // one token: already a step's queries
+  int rc = KVQ_OK;
+  if (a.T > 1) {
+    __half* steps = reinterpret_cast<__half*>(ws + p.step_q);
+    rc = check_cuda(kvq::launch_step_queries(d, a.q, steps, a.T, s));
+    q = steps;
+  }
+  kvq::DecodeWork w;
+  w.uniform = c->uniform() ? 1 : 0;
+  for (int b = 0; b < (w.uniform ? 1 : d.B); ++b) {
+    w.L[b] = c->L[b];
+    w.Q[b] = c->Q[b];
+  }
+  w.n_groups = p.steps.n_groups;
+  w.n_fp16 = p.steps.n_fp16;
+  w.splits_q = p.steps.splits_quant;
+  w.splits_f = p.steps.splits_fp16;
+  w.splits = w.splits_q + w.splits_f;
+  w.score_scale = a.score_scale;
+  w.stall = 0;
+  w.center = p.steps.centered;
+  const size_t rows = static_cast<size_t>(d.B) * d.Hq;
+  a.new_only = 1;
+  if (!rc) rc = check_cuda(kvq::launch_chunk_simple(d, cb, a, s));
+  for (int t0 = 0; t0 < a.T && !rc; t0 += kvq::kStepTokens) {
+    for (int t = t0; t < std::min(a.T, t0 + kvq::kStepTokens) && w.splits > 0 && !rc; ++t) {
+      kvq::Partials part;
+      part.status = a.status;
+      part.ml = ml + (t - t0) * rows * w.splits;
+      part.o = o + (t - t0) * rows * w.splits * d.dv;
+      rc = check_cuda(kvq::launch_decode_var(d, cb, w, q + t * rows * d.dk, part, s));
+    }
+    if (!rc) rc = check_cuda(kvq::launch_combine_steps(d, a, ml, o, w.splits, t0, s));
+  }
+  return rc;
 }
 
 }  // namespace
@@ -1193,6 +1257,8 @@ int kvq_chunk_attention(kvq_cache* c, const void* q, const void* k_new, const vo
     a.q = rq;
     a.k_new = rk;
   }
+  a.new_only = 0;
+  if (p.kernel == ChunkPlan::kSteps) return run_steps(c, p, a, ws, s);
   const kvq::CacheBufs cb = cache_bufs(c);
   rc = check_cuda((p.kernel == ChunkPlan::kFew    ? kvq::launch_chunk_few
                    : p.kernel == ChunkPlan::kTile ? kvq::launch_chunk_mma

@@ -118,7 +118,16 @@ struct ChunkArgs {
   float2* ml;             // [B * Hq * T][splits]
   float* o;               // [B * Hq * T][splits][dv]
   unsigned int* status;
+  int new_only;           // the CUDA-core kernel: the new tokens alone, as the partial of a row (splits 1)
 };
+
+// A width map's chunk runs as decode steps (one per new token) over the cached tokens, partials
+// [kStepTokens][B * Hq][splits] of kStepTokens tokens at a time (the workspace does not grow with
+// the prompt), and the CUDA-core kernel over the new ones, partials ml, o of ChunkArgs.
+constexpr int kStepTokens = 16;
+cudaError_t launch_step_queries(const Dims& d, const __half* q, __half* steps, int T, cudaStream_t s);
+cudaError_t launch_combine_steps(const Dims& d, const ChunkArgs& a, const float2* step_ml, const float* step_o,
+                                 int step_splits, int t0, cudaStream_t s);
 
 // Splits of each (b, kv head, row block) for sequences of at most L cached tokens (num_splits > 0: that
 // many, clamped to the tokens), for either kernel.

@@ -237,6 +237,26 @@ def test_chunk_cache_forms(extra, T):
     check_chunk(Twin(config(**extra), [640, 300, 127], seed=11), T, splits=(0, 2))
 
 
+@pytest.mark.parametrize("extra", [
+    VAR, dict(VAR, paged=1), dict(VAR, n_q_heads=2), dict(VAR, log_retain=0, window=0),
+    dict(k_bits=0, v_bits=0, k_widths=[8] * 32 + [2] * 96, v_widths=[4] * 64 + [2] * 64),
+    dict(k_bits=0, v_bits=0, group_v=32, k_widths=[4] * 64 + [2] * 64, v_widths=[4] * 64 + [2] * 64),
+    dict(k_bits=0, v_bits=0, group_v=16, group_k=16, k_widths=[4] * 128, v_widths=[2] * 128)])
+@pytest.mark.parametrize("T,counts", [(5, [5, 0, 2]), (17, [17, 16, 1]), (32, [32, 32, 32]), (3, [0, 0, 0])])
+def test_chunk_width_maps(extra, T, counts):
+    """The decode steps of a width map's chunk: both head groupings the decode kernel has, the maps
+    built in and others, more tokens than are merged at a time, an empty cache."""
+    lengths = [0, 640, 65] if T != 32 else [513] * 3
+    check_chunk(Twin(config(**extra), lengths, seed=T), T, counts=counts, splits=(0, 1, 3),
+                kernels=(K.KVQ_KERNEL_TENSOR,))
+
+
+@pytest.mark.parametrize("extra", [VAR, dict(VAR, n_q_heads=4)])
+def test_chunk_width_maps_by_size(extra):
+    """The automatic choice on either side of its size rule, and a head grouping of no tensor kernel."""
+    check_chunk(Twin(config(**extra, batch=1, max_context=5000), [4500], seed=5), 3)
+
+
 @pytest.mark.parametrize("T,counts", [(5, [5, 0, 2]), (40, [1, 40, 33]), (3, [0, 0, 0])])
 def test_chunk_counts_leave_the_other_rows_alone(T, counts):
     check_chunk(Twin(config(), [300, 500, 40], seed=T), T, counts=counts)
