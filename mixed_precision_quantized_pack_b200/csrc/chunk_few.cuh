@@ -1,11 +1,11 @@
-// Chunk attention with up to 16 query rows of a kv head (one or a few new tokens), and with any number
+// Chunk attention with up to 24 query rows of a kv head (one or a few new tokens), and with any number
 // over a cache with a side code, 16 at a time: the one-token
 // decode kernel's design (decode_mma.cuh) with a query row per MMA column.
 //
 // One CTA = 4 warps = one split of one (b, kv head): splits [0, splits_q) cover whole key groups of
 // the quantized prefix, the others the fp16 list followed by the new tokens.  Units (key groups, or
 // tiles of 16 fp16 rows) go round-robin to the warps through a ring of bulk-copied shared-memory
-// stages.  Scores: mma.m16n8k16 with 16 tokens on M, 8 query rows on N (one or two such n-tiles);
+// stages.  Scores: mma.m16n8k16 with 16 tokens on M, 8 query rows on N (one to three such n-tiles);
 // key codes are masked in place as fp16 subnormals (one AND per two codes), the per-channel key
 // scales are folded into the query once per group and the zero points add one MMA per k-step.
 // p.V: channels on M, tokens on K, query rows on N, weights p_j * s_{j,g} moved to the B layout with
@@ -14,9 +14,11 @@
 //
 // Where the decode kernel splits query and weights into two fp16 halves (eight columns, four rows),
 // this one rounds them to fp16 once: twice the rows for the same work.  Sums, maxima and
-// accumulators are fp32.  Bound: instruction issue (a code unpack per 8 or 16 rows), with the
-// cache's bytes not far below; the tcgen05 kernels decode to shared memory first, which 16 rows do
-// not pay for (4 tokens over 32 x 32k: 0.59 ms there).
+// accumulators are fp32.  Bound: instruction issue (a code unpack per 8 to 24 rows), with the
+// cache's bytes not far below; the tcgen05 kernels decode to shared memory first, which few rows do
+// not pay for (over 32 x 32k, 16 rows 0.42 ms here and 0.59 there, 24 rows 0.56 and 0.71; K2V2 over
+// 16 x 16k, 24 rows 0.17 and 0.33).  A fourth n-tile spills 900 bytes a thread (32 rows over
+// 32 x 32k 1.00 ms, 0.72 there).
 #pragma once
 
 #include "decode_mma.cuh"
@@ -51,7 +53,7 @@ struct Smem {
 
 template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int NT>
 struct Rings {
-  // four CTAs an SM with one n-tile, two with two: their accumulators spill at 168 registers
+  // four CTAs an SM with one n-tile, two with two or three: their accumulators spill at 168 registers
   static constexpr int CTAS = NT == 1 ? 4 : 2;
   static constexpr int AVAIL = 233472 / CTAS - 1024;
   static constexpr int HDR = Smem<DK / 16, NT, SR>::kStages;
@@ -780,7 +782,9 @@ LaunchFn find_side(const Dims& d, int rows);
 #define KVQ_CHUNK_FEW_ENTRY(KB, VB, DK, GV, GK, SR, SQ)                                        \
   if (d.kb == KB && d.vb == VB && d.dk == DK && d.gv == GV && d.gk == GK && d.sr == SR &&      \
       (SR == 0 || d.sq == SQ))                                                                 \
-    return rows <= 8 ? &launch<KB, VB, DK, GV, GK, SR, SQ, 1> : &launch<KB, VB, DK, GV, GK, SR, SQ, 2>;
+    return chunk_few_block(rows) == 8    ? &launch<KB, VB, DK, GV, GK, SR, SQ, 1>              \
+           : chunk_few_block(rows) == 16 ? &launch<KB, VB, DK, GV, GK, SR, SQ, 2>              \
+                                         : &launch<KB, VB, DK, GV, GK, SR, SQ, 3>;
 
 }  // namespace few
 }  // namespace kvq

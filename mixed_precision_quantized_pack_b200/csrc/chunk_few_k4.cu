@@ -16,7 +16,7 @@ few::LaunchFn find(const Dims& d, int T) {
   const int rows = d.n_rep * T;
   if (d.var || d.dv != few::kDV) return nullptr;
   if (d.sr) return few::find_side(d, rows);
-  if (rows > 16) return nullptr;
+  if (rows > 24) return nullptr;
   few::LaunchFn fn = few::find_4(d, rows);
   return fn ? fn : few::find_28(d, rows);
 }

@@ -134,8 +134,10 @@ cudaError_t launch_combine_steps(const Dims& d, const ChunkArgs& a, const float2
 int chunk_simple_splits(const Dims& d, int L, int T, int num_splits);
 int chunk_mma_splits(const Dims& d, int L, int T, int num_splits);
 bool chunk_mma_supported(const Dims& d);
-// One or a few new tokens, up to 16 query rows of a kv head, or a cache with a side code (chunk_few.cuh).
+// One or a few new tokens, up to 24 query rows of a kv head, or a cache with a side code (chunk_few.cuh).
 bool chunk_few_supported(const Dims& d, int T);
+// Query rows that a block of the few-row kernel takes, of `rows` in all: n-tiles of 8, up to three.
+inline int chunk_few_block(int rows) { return rows <= 8 ? 8 : rows <= 16 || rows > 24 ? 16 : 24; }
 cudaError_t launch_chunk_few(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s);
 // Up to this many query rows of a kv head the tokens take the MMA's rows (chunk_narrow.cu); with 64
 // rows the narrow kernel's softmax took 1.40 ms where the wide one takes 0.89 (32 sequences of 32k).
