@@ -17,7 +17,7 @@
 // accumulators are fp32.  Bound: instruction issue (a code unpack per 8 to 24 rows), with the
 // cache's bytes not far below; the tcgen05 kernels decode to shared memory first, which few rows do
 // not pay for (over 32 x 32k, 16 rows 0.42 ms here and 0.59 there, 24 rows 0.56 and 0.71; K2V2 over
-// 16 x 16k, 24 rows 0.17 and 0.33).  A fourth n-tile spills 900 bytes a thread (32 rows over
+// 16 x 16k, 24 rows 0.17 and 0.22).  A fourth n-tile spills 900 bytes a thread (32 rows over
 // 32 x 32k 1.00 ms, 0.72 there).
 #pragma once
 
