@@ -412,7 +412,7 @@ cudaError_t launch_append_tokens(const Dims& d, const CacheOut& c, const SeqChun
   if (max_new_groups > 0) {
     const size_t rows = static_cast<size_t>(d.gk) * (d.dk + d.dv + 2 * kPad) * 2;
     size_t smem = rows + d.dk * 12 + 4096 + d.gk * 32 + 64;
-      smem = std::max(smem, static_cast<size_t>(kMaxRetained) * (d.dk + d.dv + 2 * kPad) * 2);
+    smem = std::max(smem, static_cast<size_t>(kMaxRetained) * (d.dk + d.dv + 2 * kPad) * 2);
     static SmemLimit limit;
     const cudaError_t e = limit.raise(append_groups_kernel, static_cast<int>(smem));
     if (e != cudaSuccess) return e;

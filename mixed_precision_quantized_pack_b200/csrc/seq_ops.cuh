@@ -2,9 +2,8 @@
 // sequences: chunk attention, multi-token append, forks and page moves.
 #pragma once
 
-#include <atomic>
-
 #include "kvq_internal.cuh"
+#include "smem_limit.h"
 
 namespace kvq {
 
@@ -27,25 +26,6 @@ __device__ __forceinline__ SeqNew seq_new(const SeqChunk& w, int b, int log_reta
   s.n_ret = log_retain ? retained_count(s.Q) : 0;
   return s;
 }
-
-// A kernel's limit of dynamic shared memory on every device, raised once for the largest size asked
-// for (a call to the runtime each time costs more than the launch's argument checks).
-struct SmemLimit {
-  std::atomic<int> bytes[64] = {};
-  template <typename K>
-  cudaError_t raise(K* kernel, int need) {
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, need);
-    if (bytes[dev].load(std::memory_order_acquire) >= need) return cudaSuccess;
-    const cudaError_t e2 = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, need);
-    int have = bytes[dev].load();
-    while (e2 == cudaSuccess && have < need && !bytes[dev].compare_exchange_weak(have, need)) {
-    }
-    return e2;
-  }
-};
 
 // Quantized prefix of a sequence of L tokens.
 __host__ __device__ inline int prefix_of(const Dims& d, int L) {
