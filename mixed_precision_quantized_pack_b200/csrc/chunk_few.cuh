@@ -158,9 +158,33 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   constexpr float kMid = static_cast<float>(1 << (VB - 1));   // centre of the value codes
   const float alpha24 = a.score_scale * 16777216.0f;          // undoes the 2^-24 of subnormal codes
 
+  // Weights are 2^(score - reference + lift).  Their products with a value scale are rounded to fp16
+  // below, so `lift` puts them where fp16 is exact to 2^-11: the largest scale so far, times 2^lift, lies
+  // in [2^11, 2^15], whatever the values' magnitude (unlifted, values around 1e-4 came out with errors
+  // of a percent: their products with most weights are subnormal).  A scale above 2^(15 - lift) moves
+  // it; the smallest one there is, 2^-24, passes the initial 2^-49.  The fp16 list keeps 0: its weights
+  // are rounded without a scale.  The check costs up to 3% (units of 32 tokens; with a side code and
+  // three n-tiles 6%).
+  float lift = quant ? 64.0f : 0.0f;
+
+  auto scale_row = [&](int nt, float f0, float f1) {
+    l_run[nt][0] *= f0;
+    l_run[nt][1] *= f1;
+#pragma unroll
+    for (int g = 0; g < G::NVG; ++g) {
+      zsum[g][nt][0] *= f0;
+      zsum[g][nt][1] *= f1;
+    }
+#pragma unroll
+    for (int mv = 0; mv < 8; ++mv) {
+      co[nt][mv][0] *= f0;
+      co[nt][mv][1] *= f1;
+      co[nt][mv][2] *= f0;
+      co[nt][mv][3] *= f1;
+    }
+  };
   // Moves the references of an n-tile's rows to their maxima.  They do not lag behind: weights stay at
-  // most 1, and their products with a value scale, rounded to fp16 below, within its range (a lag
-  // of 8 measured 4% less time at most).
+  // most 2^lift, and those products at most 2^15 (a lag of 8 measured 4% less time at most).
   auto rescale = [&](int nt, float g0, float g1) {
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
@@ -172,20 +196,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
       const float f0 = mv0 ? ptx::ex2(m_run[nt][0] - g0) : 1.0f, f1 = mv1 ? ptx::ex2(m_run[nt][1] - g1) : 1.0f;
       if (mv0) m_run[nt][0] = g0;
       if (mv1) m_run[nt][1] = g1;
-      l_run[nt][0] *= f0;
-      l_run[nt][1] *= f1;
-#pragma unroll
-      for (int g = 0; g < G::NVG; ++g) {
-        zsum[g][nt][0] *= f0;
-        zsum[g][nt][1] *= f1;
-      }
-#pragma unroll
-      for (int mv = 0; mv < 8; ++mv) {
-        co[nt][mv][0] *= f0;
-        co[nt][mv][1] *= f1;
-        co[nt][mv][2] *= f0;
-        co[nt][mv][3] *= f1;
-      }
+      scale_row(nt, f0, f1);
     }
   };
 
@@ -431,6 +442,25 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
             if (off == 16 * mt + qr + 8) sc[nt][mt][2] = sc[nt][mt][3] = -INFINITY;
           }
       }
+      // ---- the lift of the weights follows the group's value scales ----
+      {
+        constexpr int W = GK * G::NVG / 32;      // the lane's share of the (scale, zero) pairs
+        uint32_t sz[W];
+        mma::load_words<W>(svm + lane * W, sz);
+        __half2 mx = ptx::u32_as_h2(sz[0]);
+#pragma unroll
+        for (int i = 1; i < W; ++i) mx = __hmax2(mx, ptx::u32_as_h2(sz[i]));
+        float top = __low2float(mx);
+        if (__any_sync(0xffffffffu, top > ptx::ex2(15.0f - lift))) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;      // 2^e <= top < 2^(e + 1)
+          const float to = static_cast<float>(11 - e), f = ptx::ex2(to - lift);
+          lift = to;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) scale_row(nt, f, f);
+        }
+      }
       // ---- online softmax update for the group ----
       float m_use[NT][2];
 #pragma unroll
@@ -443,7 +473,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
         }
         rescale(nt, x0, x1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) m_use[nt][i] = m_run[nt][i] == -INFINITY ? 0.0f : m_run[nt][i];
+        for (int i = 0; i < 2; ++i) m_use[nt][i] = (m_run[nt][i] == -INFINITY ? 0.0f : m_run[nt][i]) - lift;
       }
 
       // ---- p.V over the group ----
@@ -720,7 +750,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
         dst[c1] = failed ? 0.0f : o1;
       }
       if (qr == 0) {
-        sm_ml[(warp * NR + r) * 2] = m_run[nt][i];
+        sm_ml[(warp * NR + r) * 2] = m_run[nt][i] - lift;      // -inf stays -inf
         sm_ml[(warp * NR + r) * 2 + 1] = l_run[nt][i];
       }
     }
