@@ -87,6 +87,15 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   const SeqNew sw = seq_new(a.seq, b, d.log_retain);
   if (sw.n == 0) return;
   const int n_rows = d.n_rep * a.T;
+  // the new tokens that some row of the block may see; none of its rows may be valid
+  int n_vis = sw.n;
+  {
+    const int r1 = min(rb + 8 * NT, n_rows) - 1;
+    if (rb / a.T == r1 / a.T) {                 // rows of one head: tokens rb % T to r1 % T
+      if (rb % a.T >= sw.n) return;
+      if (!a.mask) n_vis = min(n_vis, r1 % a.T + 1);
+    }
+  }
 
   uint32_t* sm_qb = reinterpret_cast<uint32_t*>(smem + SM::kQb);
   uint32_t* sm_qf = reinterpret_cast<uint32_t*>(smem + SM::kQf);
@@ -120,7 +129,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   }
 
   // ---------------- work list of this CTA ----------------
-  const int n_old = sw.n_ret + sw.L - sw.Q, n_list = n_old + sw.n;     // the fp16 list, then the new tokens
+  const int n_old = sw.n_ret + sw.L - sw.Q, n_list = n_old + n_vis;    // the fp16 list, then the new tokens
   int unit_begin, unit_end, list_begin = 0, list_end = 0;
   if (quant) {
     const long long groups = sw.Q / GK;

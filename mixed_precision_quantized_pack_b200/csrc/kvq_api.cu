@@ -1173,7 +1173,18 @@ int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
     const int rc = plan_counts(d, nG, nF, c->sm_count, num_splits, true, &plan);
     if (rc) return rc;
     p->splits_q = plan.splits_quant;
-    p->splits = plan.splits_quant + plan.splits_fp16;
+    // The decode planner splits the fp16 list, with the new tokens in it, by its bytes and for one row
+    // block.  Where there are several (a side code) their CTAs come first: the list is split only while
+    // CTAs are short, so that neither they nor the partials grow with the square of T (8192 tokens
+    // behind 700, rank 4: 10.2 -> 0.27 GB).
+    int list = plan.splits_fp16;
+    const int block = kvq::chunk_few_block(d.n_rep * T);
+    const long long blocks = (static_cast<long long>(d.n_rep) * T + block - 1) / block;
+    if (blocks > 1 && (num_splits == 0 || nG > 0)) {
+      const long long ctas = (block == 8 ? 4LL : 2LL) * c->sm_count / (blocks * d.B * d.Hkv) - p->splits_q;
+      list = static_cast<int>(std::max(1LL, std::min<long long>(list, ctas)));
+    }
+    p->splits = p->splits_q + list;
   } else if (p->kernel == ChunkPlan::kSteps) {
     p->splits = 1;
     const int rc = plan_cache(c, num_splits, true, &p->steps);

@@ -5,9 +5,23 @@ import pytest
 import torch
 
 from mixed_precision_quantized_pack_b200 import kvq as K
-from test_gpu_seq_ops import KERNELS, VAR, Twin, check_chunk, config
+import test_gpu_seq_ops as seq_ops
+from test_gpu_seq_ops import KERNELS, Twin, check_chunk, config
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _reference_of_no_rows(monkeypatch):
+    """The plain form of a sequence without new tokens: no rows (its side-code term takes one at least)."""
+    full = seq_ops.reference
+
+    def reference(tw, b, q, k_new, v_new, sees):
+        if q.shape[1] == 0:
+            empty = np.zeros(q.shape[:2] + (tw.cfg["d_v"],))
+            return empty, empty
+        return full(tw, b, q, k_new, v_new, sees)
+    monkeypatch.setattr(seq_ops, "reference", reference)
 
 
 class Scaled(Twin):
@@ -51,3 +65,33 @@ def test_chunk_values_that_grow():
             tw.oc[b].prefill(k[None], v[None])
         for T in (1, 4, 6):
             check_chunk(tw, T, splits=(0, 1, 3), kernels=KERNELS[:1])
+
+
+@pytest.mark.parametrize("T,counts,masked", [(200, [200, 131, 7], False), (90, [90, 0, 89], True), (17, [17, 1, 16], False)])
+def test_chunk_side_code_prompts(T, counts, masked):
+    """Many row blocks over a side code: blocks that see few of the new tokens, blocks of rows behind
+    the valid ones, blocks across two heads, an empty cache."""
+    tw = Twin(config(side_rank=4, side_bits=4), [0, 640, 300], seed=T)
+    sees = None
+    if masked:
+        rng = np.random.default_rng(T)
+        sees = [rng.random((T, T)) < 0.2 for _ in range(3)]
+    check_chunk(tw, T, counts=counts, sees=sees, splits=(0, 1, 3), kernels=KERNELS[:1])
+    check_chunk(Twin(config(side_rank=8, side_bits=4, n_q_heads=2), [129, 0, 5], seed=T), T, counts=counts, sees=sees,
+                kernels=KERNELS[:1])
+
+
+def test_chunk_workspace_is_linear_in_the_new_tokens():
+    """Two partials a row and no more once the rows fill the GPU, whatever stands in the cache; below
+    that, what the splits of a few CTAs an SM leave."""
+    for batch, L in ((1, 0), (1, 700), (8, 700), (2, 9000)):
+        tw = Twin(config(batch=batch, n_q_heads=32, n_kv_heads=8, max_context=32768, side_rank=4, side_bits=4), [0] * batch)
+        if L:
+            k = torch.randn((batch, 8, L, 128), device="cuda").half()
+            tw.gc.prefill(k, k)
+        for T in (1, 4, 16, 100, 1024, 4096, 8192, 65536):
+            for splits in (0, 8):
+                partial = batch * 32 * T * (128 + 2) * 4
+                size = K.kvq_chunk_workspace_size(tw.gc.handle, T, splits)
+                assert size <= partial * max(2, splits + 1) + (32 << 20), (batch, L, T, splits, size)
+        tw.gc.close()
