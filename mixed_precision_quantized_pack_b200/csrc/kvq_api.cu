@@ -1212,9 +1212,9 @@ int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
   return KVQ_OK;
 }
 
-// A width map's chunk: the one-token decode kernel for every new token's queries over the cached
-// tokens, the new tokens on CUDA cores, one merge.
-int run_steps(const kvq_cache* c, const ChunkPlan& p, kvq::ChunkArgs& a, char* ws, cudaStream_t s) {
+// A width map's chunk: the one-token decode kernel for the queries of every new token (up to the most a
+// sequence has) over the cached tokens, the new tokens on CUDA cores, one merge.
+int run_steps(const kvq_cache* c, const ChunkPlan& p, kvq::ChunkArgs& a, int most, char* ws, cudaStream_t s) {
   const kvq::Dims& d = c->d;
   const kvq::CacheBufs cb = cache_bufs(c);
   float2* ml = reinterpret_cast<float2*>(ws + p.step_ml);
@@ -1243,8 +1243,8 @@ int run_steps(const kvq_cache* c, const ChunkPlan& p, kvq::ChunkArgs& a, char* w
   const size_t rows = static_cast<size_t>(d.B) * d.Hq;
   a.new_only = 1;
   if (!rc) rc = check_cuda(kvq::launch_chunk_simple(d, cb, a, s));
-  for (int t0 = 0; t0 < a.T && !rc; t0 += kvq::kStepTokens) {
-    for (int t = t0; t < std::min(a.T, t0 + kvq::kStepTokens) && w.splits > 0 && !rc; ++t) {
+  for (int t0 = 0; t0 < most && !rc; t0 += kvq::kStepTokens) {
+    for (int t = t0; t < std::min(most, t0 + kvq::kStepTokens) && w.splits > 0 && !rc; ++t) {
       kvq::Partials part;
       part.status = a.status;
       part.ml = ml + (t - t0) * rows * w.splits;
@@ -1287,6 +1287,8 @@ int kvq_chunk_attention(kvq_cache* c, const void* q, const void* k_new, const vo
   kvq::ChunkArgs a;
   rc = seq_chunk(c, T, counts, &a.seq);
   if (rc) return rc;
+  const int most = counts ? *std::max_element(counts, counts + d.B) : T;
+  if (most == 0) return KVQ_OK;               // no row to write
   DeviceScope on(c->device);
   if (!on.ok) return KVQ_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1314,7 +1316,7 @@ int kvq_chunk_attention(kvq_cache* c, const void* q, const void* k_new, const vo
     a.k_new = rk;
   }
   a.new_only = 0;
-  if (p.kernel == ChunkPlan::kSteps) return run_steps(c, p, a, ws, s);
+  if (p.kernel == ChunkPlan::kSteps) return run_steps(c, p, a, most, ws, s);
   const kvq::CacheBufs cb = cache_bufs(c);
   rc = check_cuda((p.kernel == ChunkPlan::kFew    ? kvq::launch_chunk_few
                    : p.kernel == ChunkPlan::kTile ? kvq::launch_chunk_mma

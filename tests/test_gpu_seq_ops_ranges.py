@@ -1,12 +1,14 @@
 """Chunk attention where the values are small, where a CTA walks many tiles, and where calls are
 padded or long: what the split and row-block plans do there, and the workspace they ask for."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from mixed_precision_quantized_pack_b200 import kvq as K
 import test_gpu_seq_ops as seq_ops
-from test_gpu_seq_ops import KERNELS, Twin, check_chunk, config
+from test_gpu_seq_ops import KERNELS, VAR, Twin, check_chunk, config
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +97,33 @@ def test_chunk_workspace_is_linear_in_the_new_tokens():
                 size = K.kvq_chunk_workspace_size(tw.gc.handle, T, splits)
                 assert size <= partial * max(2, splits + 1) + (32 << 20), (batch, L, T, splits, size)
         tw.gc.close()
+
+
+def launches(call):
+    """Graph nodes that a captured call leaves."""
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        call()
+    n = ctypes.c_size_t()
+    assert ctypes.CDLL("libcuda.so.1").cuGraphGetNodes(ctypes.c_void_p(g.raw_cuda_graph()), None, ctypes.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
+@pytest.mark.parametrize("extra", [VAR, dict(), dict(side_rank=4, side_bits=4, rot_keys=1)])
+def test_chunk_padding_is_not_worked_through(extra):
+    """A chunk padded to more tokens than any sequence brings costs a width map no further passes over
+    the cache, and one without a token no launch at all."""
+    tw = Twin(config(**extra), [640, 300, 513], seed=6)
+    gc = tw.gc
+    gc.set_kernel(K.KVQ_KERNEL_TENSOR)
+
+    def count(T, counts):
+        q, k, v = [torch.from_numpy(x).cuda() for x in tw.chunk(T)]
+        out = torch.zeros((3, 8, T, 128), dtype=torch.float16, device="cuda")
+        return launches(lambda: gc.chunk_attention(q, k, v, counts=counts, out=out))
+    assert count(40, [0, 0, 0]) == 0
+    assert count(40, [3, 0, 2]) <= count(3, [3, 0, 2]) + 1          # (one more to reorder the queries)
+    assert count(40, [18, 0, 2]) <= count(18, [18, 0, 2]) + 1
+    check_chunk(tw, 40, counts=[18, 0, 2], kernels=(K.KVQ_KERNEL_TENSOR,))
+    check_chunk(tw, 40, counts=[3, 1, 2], kernels=(K.KVQ_KERNEL_TENSOR,))
