@@ -17,8 +17,10 @@
 // accumulators are fp32.  Bound: instruction issue (a code unpack per 8 to 24 rows), with the
 // cache's bytes not far below; the tcgen05 kernels decode to shared memory first, which few rows do
 // not pay for (over 32 x 32k, 16 rows 0.42 ms here and 0.59 there, 24 rows 0.56 and 0.71; K2V2 over
-// 16 x 16k, 24 rows 0.17 and 0.22).  A fourth n-tile spills 900 bytes a thread (32 rows over
-// 32 x 32k 1.00 ms, 0.72 there).
+// 16 x 16k, 24 rows 0.17 and 0.22; K4V4 0.18 and 0.20).  Groups of 32 with 4-bit keys and 2-bit values
+// are about even at 17 to 24 rows (20 rows, 8 kv heads: 4 x 32k 111 us here and 131 there, 12 x 2k 46
+// and 66, 8 x 16k 124 and 125; 16 x 16k 221 and 214, 12 x 8k 133 and 113, 16 x 2k 66 and 55).  A fourth
+// n-tile spills 900 bytes a thread (32 rows over 32 x 32k 1.00 ms, 0.72 there).
 #pragma once
 
 #include "decode_mma.cuh"
@@ -821,8 +823,8 @@ LaunchFn find_side(const Dims& d, int rows);
 #define KVQ_CHUNK_FEW_ENTRY(KB, VB, DK, GV, GK, SR, SQ)                                        \
   if (d.kb == KB && d.vb == VB && d.dk == DK && d.gv == GV && d.gk == GK && d.sr == SR &&      \
       (SR == 0 || d.sq == SQ))                                                                 \
-    return chunk_few_block(rows) == 8    ? &launch<KB, VB, DK, GV, GK, SR, SQ, 1>              \
-           : chunk_few_block(rows) == 16 ? &launch<KB, VB, DK, GV, GK, SR, SQ, 2>              \
+    return chunk_few_block(d, rows) == 8    ? &launch<KB, VB, DK, GV, GK, SR, SQ, 1>              \
+           : chunk_few_block(d, rows) == 16 ? &launch<KB, VB, DK, GV, GK, SR, SQ, 2>              \
                                          : &launch<KB, VB, DK, GV, GK, SR, SQ, 3>;
 
 }  // namespace few

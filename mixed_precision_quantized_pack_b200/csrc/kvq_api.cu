@@ -1105,7 +1105,7 @@ struct ChunkPlan {
 // 16 rows, against the decode's planner (three CTAs per SM): 4 x 32k 68 and 89 us, 16 x 16k 130 and
 // 162, 64 x 2k 130 and 176.
 int few_splits(const kvq::Dims& d, int nG, double mean, int nF, int rows, int sm_count) {
-  const int block = kvq::chunk_few_block(rows);
+  const int block = kvq::chunk_few_block(d, rows);
   const double units = static_cast<double>(d.B) * d.Hkv * ((rows + block - 1) / block);
   const double sms = sm_count, fixed = block == 8 ? 512.0 : 256.0, list = nF + fixed;
   const int hi = std::min(nG, split_cap(d));
@@ -1178,7 +1178,7 @@ int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
     // CTAs are short, so that neither they nor the partials grow with the square of T (8192 tokens
     // behind 700, rank 4: 10.2 -> 0.27 GB).
     int list = plan.splits_fp16;
-    const int block = kvq::chunk_few_block(d.n_rep * T);
+    const int block = kvq::chunk_few_block(d, d.n_rep * T);
     const long long blocks = (static_cast<long long>(d.n_rep) * T + block - 1) / block;
     if (blocks > 1 && (num_splits == 0 || nG > 0)) {
       const long long ctas = (block == 8 ? 4LL : 2LL) * c->sm_count / (blocks * d.B * d.Hkv) - p->splits_q;

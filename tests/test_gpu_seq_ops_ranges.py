@@ -83,6 +83,16 @@ def test_chunk_side_code_prompts(T, counts, masked):
                 kernels=KERNELS[:1])
 
 
+@pytest.mark.parametrize("kb", [2, 4])
+@pytest.mark.parametrize("rank,bits", [(4, 4), (4, 8), (8, 4)])
+def test_chunk_side_code_up_to_24_rows(kb, rank, bits):
+    """17 to 24 query rows over a side code: two blocks of rows for a few sequences, one for more."""
+    for batch, lengths in ((3, [700, 129, 400]), (13, [300, 130, 0, 513] + [200 + 7 * i for i in range(9)])):
+        tw = Twin(config(batch=batch, side_rank=rank, side_bits=bits, k_bits=kb), lengths, seed=batch)
+        for T in (5, 6):
+            check_chunk(tw, T, splits=(0, 1), kernels=KERNELS[:1])
+
+
 def test_chunk_workspace_is_linear_in_the_new_tokens():
     """Two partials a row and no more once the rows fill the GPU, whatever stands in the cache; below
     that, what the splits of a few CTAs an SM leave."""
