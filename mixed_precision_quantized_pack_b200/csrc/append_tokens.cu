@@ -39,7 +39,9 @@ __device__ __forceinline__ TokenSource token_source(const Dims& d, const __half*
     const int i = p - s.L;
     int r = index ? index[static_cast<long long>(b) * T + i] : i;
     if (r < 0 || r >= T) r = 0;               // an index outside the chunk reads its first row
-    t.base = fresh + (static_cast<long long>(bh) * T + r) * width;
+    long long row = static_cast<long long>(bh) * T + r;
+    if (!KVQ_IN_BOUNDS(d, kSiteTokSrc, row, static_cast<long long>(d.B) * d.Hkv * T)) row = 0;
+    t.base = fresh + row * width;
   }
   return t;
 }
@@ -52,13 +54,6 @@ __device__ __forceinline__ void rotate_smem_row(__half* row, const Dims& d, int 
 #pragma unroll
   for (int m = 0; m < 8; ++m)
     if (m < d.dk / 32) row[lane + 32 * m] = __float2half_rn(x[m]);
-}
-
-// Half index of (scale, zero) of channel c in a fixed-width key group's block.
-__device__ __forceinline__ int key_slot(int c, int dk, int kb) {
-  const int per = 32 / kb, half = per / 2, words = dk / per, quarter = words % 4 == 0 ? words / 4 : 0;
-  const int w = c / per, r = c % per, pos = quarter ? (w % quarter) * 4 + w / quarter : w;
-  return pos * 2 * per + (r % half) * 2 + r / half;
 }
 
 // Codes of 8 fp16 values, LSB first; prm(j) is (zero, 1 / scale, scale) of value j's group.  The

@@ -33,8 +33,7 @@ constexpr float kOver = kLazy + kBias;        // (references are kept with kBias
 
 template <int DK, int N>
 struct Layout {
-  static constexpr int NT = 256;                          // producer threads
-  static constexpr int kThreads = kSoftmaxThreads + NT + 64;   // and a warp that copies, one that issues the MMAs
+  static constexpr int kThreads = kSoftmaxThreads + kProducers + 64;   // and a warp that copies, one that issues the MMAs
   static constexpr int KH = DK > 64 ? DK / 64 : 1;
   static constexpr int kK = 0;
   static constexpr int kV = kK + 2 * KH * kHalf;
@@ -122,7 +121,7 @@ chunk_narrow_kernel(const __grid_constant__ Dims d, const __grid_constant__ Cach
   float* sm_w = reinterpret_cast<float*>(sm_t + N);             // [4][N] per warp: maxima, in the end sums
   const uint32_t bars = base + Lay::kBars;
   if (tid == 0) {
-    init_token_bars(bars, Lay::NT / 32, Lay::NT / 32, 1);
+    init_token_bars(bars, kProducers / 32, kProducers / 32, 1);
     for (int i = 0; i < 2; ++i) ptx::mbar_init(bars + 8 * (kSFull + i), 1);
     ptx::mbar_init(bars + 8 * kPFull, kSoftmaxThreads / 32);
     ptx::mbar_init(bars + 8 * kPvDone, 1);
@@ -145,7 +144,7 @@ chunk_narrow_kernel(const __grid_constant__ Dims d, const __grid_constant__ Cach
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t to = tmem + 2 * N + lanes;
 
-  constexpr int kCopyWarp = (kSoftmaxThreads + Lay::NT) / 32, kMmaWarp = kCopyWarp + 1;
+  constexpr int kCopyWarp = (kSoftmaxThreads + kProducers) / 32, kMmaWarp = kCopyWarp + 1;
   if (warp == kCopyWarp) {
     const Ctx c{d, cb, a, s, b, h, bh, __ffs(d.gk) - 1, __ffs(d.gv) - 1, __ffs(d.nvg) - 1,
                 base + Lay::kRing, base + Lay::kPages, stages};
@@ -198,8 +197,8 @@ chunk_narrow_kernel(const __grid_constant__ Dims d, const __grid_constant__ Cach
                 base + Lay::kRing, base + Lay::kPages, stages};
     const int pt = tid - kSoftmaxThreads;
     with_bits(d, [&](auto kb, auto vb) {
-      copy_queries<kb.value, DK, N, Lay::NT>(c, r0, n_rows, pt, base + Lay::kQ);
-      produce<kb.value, vb.value, DK, Lay::NT, false>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
+      copy_queries<kb.value, DK, N>(c, r0, n_rows, pt, base + Lay::kQ);
+      produce<kb.value, vb.value, DK, false>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
     });
     __syncthreads();
   } else {

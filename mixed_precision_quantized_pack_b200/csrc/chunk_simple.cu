@@ -124,10 +124,8 @@ chunk_simple_kernel(Dims d, CacheBufs cb, const __grid_constant__ ChunkArgs a) {
           const uint32_t code = (kr[kf[j] >> 16] >> ((kf[j] >> 8) & 31u)) & ((1u << (kf[j] & 15u)) - 1u);
           int at = 2 * ch, to_zero = 1;
           if (!d.var) {     // the paired, quarter-interleaved block of a fixed-width group
-            const int per = 32 / d.kb, half = per / 2, words = d.dk / per, quarter = words % 4 == 0 ? words / 4 : 0;
-            const int wd = ch / per, r = ch % per, pos = quarter ? (wd % quarter) * 4 + wd / quarter : wd;
-            at = pos * 2 * per + (r % half) * 2 + r / half;
-            to_zero = per;
+            at = key_slot(ch, d.dk, d.kb);
+            to_zero = 32 / d.kb;
           }
           kh[j] = fmaf(static_cast<float>(code), __half2float(ks[at]), __half2float(ks[at + to_zero]));
         }

@@ -14,10 +14,10 @@
 // free: queries and fp16 rows are written in that order too, and the order of the value channels
 // is undone where outputs are stored.  Per pair: one LOP3 (1024 + code), one exact operation that
 // removes the 1024 and the field's offset, one fused multiply-add that rounds code * s + z to
-// fp16 once.  Tokens behind the end of the prefix in its last tile repeat the last row: their
-// weights are 0 and their values finite.
-//
-// NT, here and below, is the number of threads that share a tile's keys or values (256).
+// fp16 once.  A prefix may end inside its last tile: the rest of that stage holds codes of an older
+// tile, or whatever shared memory held.  Its scores are masked before use and its weights are 0; its
+// values are finite because the values' (scale, zero) area is cleared in the beginning (clear_ring)
+// and holds nothing but finite pairs afterwards.
 #pragma once
 
 #include <algorithm>
@@ -32,6 +32,7 @@ namespace chunk {
 
 constexpr int kTile = 128;                    // tokens per tile; also the value channels
 constexpr int kHalf = kTile * 128;            // bytes of 128 rows of 64 fp16 channels
+constexpr int kProducers = 256;               // threads that decode a tile
 constexpr int kMaxRing = 4;                   // stages of the packed ring, at most
 constexpr int kMetaBytes = 4096;              // (scale, zero) of a tile: keys 2 KB, values 2 KB
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -229,10 +230,10 @@ __device__ __forceinline__ bool block_tiles(const ChunkArgs& a, const SeqNew& s,
   return true;
 }
 
-// Position of word w of a key row in its group's (scale, zero) block (quarter-interleaved when 4
-// divides the row's W words), and the word at a position.
+// Position of word w of a key row of W words in its group's (scale, zero) block, and the word at a
+// position.
 template <int W>
-__host__ __device__ constexpr int block_pos(int w) { return W % 4 == 0 ? w % (W / 4) * 4 + w / (W / 4) : w; }
+__host__ __device__ constexpr int block_pos(int w) { return key_block_pos(W, w); }
 template <int W>
 __host__ __device__ constexpr int block_word(int p) { return W % 4 == 0 ? p % 4 * (W / 4) + p / 4 : p; }
 
@@ -247,14 +248,14 @@ __host__ __device__ constexpr int key_chunk(int j) {
 // order of the (scale, zero) blocks and write them in that order too: threads then read
 // neighbouring blocks and write neighbouring chunks, and the order of the channels of a dot
 // product is free (key_chunk() gives it to the queries and fp16 rows).
-template <int KB, int DK, int NT>
+template <int KB, int DK>
 struct KeyUnits {
   static __host__ __device__ constexpr int unit(int e) { return KB == 8 ? e : block_word<DK * KB / 32>(e); }
   static constexpr int kPerRow = KB == 2 ? DK / 16 : DK / 8;
   static constexpr int kWords = KB == 8 ? 2 : 1;
-  static constexpr int kStep = NT / kPerRow < kTile ? NT / kPerRow : kTile;      // at 512 threads a thread may have none
+  static constexpr int kStep = kProducers / kPerRow;
   static constexpr int kTokens = kTile / kStep;
-  static constexpr int kThreads = kPerRow * kStep;
+  static_assert(kStep <= kTile, "every thread has tokens");
 };
 
 // What the producers of a CTA share.
@@ -275,11 +276,10 @@ __host__ __device__ constexpr int ring_stage_bytes(int kb, int vb, int dk) {
 }
 
 // The thread's codes of the key tile in the ring stage `src` to fp16 rows at `dst`.
-template <int KB, int DK, int NT>
+template <int KB, int DK>
 __device__ __forceinline__ void decode_keys(const Ctx& c, int tid, uint32_t src, uint32_t meta, uint32_t dst) {
-  using U = KeyUnits<KB, DK, NT>;
+  using U = KeyUnits<KB, DK>;
   constexpr int P = 32 / KB, W = DK / P, kRow = DK * KB / 8;
-  if (NT > U::kThreads && tid >= U::kThreads) return;
   const int u = tid % U::kPerRow, sub = tid / U::kPerRow;
   // (scale, zero) pairs of the unit, reloaded where the next group may begin
   constexpr int R = U::kWords * P / 2;
@@ -383,12 +383,12 @@ __device__ __forceinline__ void decode_keys(const Ctx& c, int tid, uint32_t src,
   }
 }
 
-// Values: a thread decodes 64 (NT 256) or 32 (512) channels of a token, in two blocks.  Threads
-// of a row's second half take their blocks in the opposite order, so that the eight threads of a
-// store phase write eight different bank groups.
-template <int VB, int NT>
+// Values: a thread decodes 64 channels of a token, in two blocks.  Threads of a row's second half
+// take their blocks in the opposite order, so that the eight threads of a store phase write eight
+// different bank groups.
+template <int VB>
 __device__ __forceinline__ void decode_values(const Ctx& c, int tid, uint32_t src, uint32_t meta, uint32_t dst) {
-  constexpr int kPerRow = NT / kTile, kChannels = kTile / kPerRow;       // threads a token, channels a thread
+  constexpr int kPerRow = kProducers / kTile, kChannels = kTile / kPerRow;       // threads a token, channels a thread
   constexpr int C = kChannels / 16, B = kChannels / 2 * VB / 32;         // chunks and words of a block
   const int e = tid % kPerRow, t = tid / kPerRow, flip = e >= kPerRow / 2;
   const uint32_t row = meta + ((t << c.lnvg) * 4);
@@ -453,11 +453,11 @@ __device__ __forceinline__ void decode_values(const Ctx& c, int tid, uint32_t sr
 
 // fp16 rows of the list (kind 1) or of the new tokens (kind 2) to a tile; entries from `n` on are zero.
 // WIDTH channels a row; the channel order is that of BITS-bit codes.
-template <int BITS, int WIDTH, int NT>
+template <int BITS, int WIDTH>
 __device__ __forceinline__ void copy_rows(const Ctx& c, bool keys, int kind, int e0, int n, int tid, uint32_t dst) {
-  constexpr int per_row = WIDTH / 16, step = NT / per_row < kTile ? NT / per_row : kTile, tokens = kTile / step;
+  constexpr int per_row = WIDTH / 16, step = kProducers / per_row, tokens = kTile / step;
+  static_assert(step <= kTile, "every thread has rows");
   const int u = tid % per_row, sub = tid / per_row;
-  if (NT > per_row * step && sub >= kTile) return;
   const __half* ret = keys ? c.cb.ret_k : c.cb.ret_v;
   const __half* win = keys ? c.cb.win_k : c.cb.win_v;
   const __half* fresh = keys ? c.a.k_new : c.a.v_new;
@@ -495,9 +495,9 @@ __device__ __forceinline__ void copy_rows(const Ctx& c, bool keys, int kind, int
 
 // ROWS query rows from r0 of the kv head's block (rows of T tokens per head; those behind the
 // sequence's new tokens are zero), in the keys' channel order.
-template <int KB, int DK, int ROWS, int NT>
+template <int KB, int DK, int ROWS>
 __device__ __forceinline__ void copy_queries(const Ctx& c, int r0, int n_rows, int tid, uint32_t dst) {
-  constexpr int per_row = DK / 16, step = NT / per_row;
+  constexpr int per_row = DK / 16, step = kProducers / per_row;
   const int u = tid % per_row, sub = tid / per_row;
   const __half* q = c.a.q + static_cast<long long>(c.bh) * n_rows * DK;
   for (int t = sub; t < ROWS; t += step) {
@@ -658,10 +658,10 @@ __device__ __forceinline__ void copy_tiles(const Ctx& c, const Tiles& t, int lan
   copier.drain(c, lane, bars, false);
 }
 
-// The loop of NT producer threads: tiles t.begin .. t.end of the CTA into stages 0, 1, 0, ... of K and
+// The loop of the producer threads: tiles t.begin .. t.end of the CTA into stages 0, 1, 0, ... of K and
 // V.  SELF: the first warp copies the packed tiles as well.  (Two groups of 256, one for the keys
 // and one for the values, gained 6% with 16 queries and lost 11% with 32.)
-template <int KB, int VB, int DK, int NT, bool SELF>
+template <int KB, int VB, int DK, bool SELF>
 __device__ __forceinline__ void produce(const Ctx& c, const Tiles& t, int tid, uint32_t kdst0, uint32_t vdst0,
                                         uint32_t bars, const Waiter& wait) {
   constexpr int kKeyStage = (DK > 64 ? DK / 64 : 1) * kHalf;
@@ -693,17 +693,17 @@ __device__ __forceinline__ void produce(const Ctx& c, const Tiles& t, int tid, u
     live = ready(kKEmpty + st, ph);
     if (!live) break;
     if (it < packed) {
-      if constexpr (kPacked) decode_keys<KB, DK, NT>(c, tid, src, src + kTile * (kRowK + kRowV), kdst);
+      if constexpr (kPacked) decode_keys<KB, DK>(c, tid, src, src + kTile * (kRowK + kRowV), kdst);
     } else {
-      copy_rows<KB, DK, NT>(c, true, kind, e0, ne, tid, kdst);
+      copy_rows<KB, DK>(c, true, kind, e0, ne, tid, kdst);
     }
     arrive(kKFull + st);
     live = ready(kVEmpty + st, ph);
     if (!live) break;
     if (it < packed) {
-      if constexpr (kPacked) decode_values<VB, NT>(c, tid, src + kTile * kRowK, src + kTile * (kRowK + kRowV) + kMetaBytes / 2, vdst);
+      if constexpr (kPacked) decode_values<VB>(c, tid, src + kTile * kRowK, src + kTile * (kRowK + kRowV) + kMetaBytes / 2, vdst);
     } else {
-      copy_rows<VB, kTile, NT>(c, false, kind, e0, ne, tid, vdst);
+      copy_rows<VB, kTile>(c, false, kind, e0, ne, tid, vdst);
     }
     arrive(kVFull + st);
     if (kPacked && it < packed) {

@@ -30,8 +30,7 @@ namespace {
 using namespace chunk;
 
 constexpr int kSoftmaxThreads = 256;          // two streams of four warps
-constexpr int kProducerThreads = 256;
-constexpr int kThreads = kSoftmaxThreads + kProducerThreads;    // 16 warps: 128 registers a thread
+constexpr int kThreads = kSoftmaxThreads + kProducers;    // 16 warps: 128 registers a thread
 
 template <int DK, int MT>
 struct Layout {
@@ -177,7 +176,7 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
 
   const uint32_t bars = base + Lay::kBars;
   if (tid == 0) {
-    init_token_bars(bars, kProducerThreads / 32, kProducerThreads / 32, MT);   // with two row tiles both streams use a tile
+    init_token_bars(bars, kProducers / 32, kProducers / 32, MT);   // with two row tiles both streams use a tile
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars + 8 * (kSFull + i), 1);
       ptx::mbar_init(bars + 8 * (kODone + i), 1);
@@ -207,8 +206,8 @@ chunk_wide_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheB
                 base + Lay::kRing, base + Lay::kPages, stages};
     with_bits(d, [&](auto kb, auto vb) {
       for (int i = 0; i < MT; ++i)
-        copy_queries<kb.value, DK, kTile, kProducerThreads>(c, r0 + i * kTile, n_rows, pt, base + Lay::kQ + i * Lay::KH * kHalf);
-      produce<kb.value, vb.value, DK, kProducerThreads, true>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
+        copy_queries<kb.value, DK, kTile>(c, r0 + i * kTile, n_rows, pt, base + Lay::kQ + i * Lay::KH * kHalf);
+      produce<kb.value, vb.value, DK, true>(c, t, pt, base + Lay::kK, base + Lay::kV, bars, wait);
     });
   } else {
     const uint32_t ts = tmem + stream * kTile + lanes, to = tmem + 2 * kTile + stream * kTile + lanes;

@@ -34,6 +34,18 @@ __host__ __device__ inline int prefix_of(const Dims& d, int L) {
   return over > 0 ? over / d.gk * d.gk : 0;
 }
 
+// Position of word w of a key row of `words` words in its group's (scale, zero) block: the words'
+// parts stand in the order of the row, or quarter-interleaved where 4 divides them.
+__host__ __device__ constexpr int key_block_pos(int words, int w) {
+  return words % 4 == 0 ? w % (words / 4) * 4 + w / (words / 4) : w;
+}
+// Half index of the scale of channel c in a fixed-width key group's block; its zero is 32 / kb
+// further on.
+__host__ __device__ constexpr int key_slot(int c, int dk, int kb) {
+  const int per = 32 / kb, half = per / 2, r = c % per;
+  return key_block_pos(dk / per, c / per) * 2 * per + (r % half) * 2 + r / half;
+}
+
 // Whether position p < Q is one of the retained tokens of a quantized prefix of Q tokens.
 __device__ __forceinline__ bool is_retained(int Q, int p) {
   return (p & ((1 << (31 - __clz(Q - p))) - 1)) == 0;
@@ -129,7 +141,7 @@ inline int chunk_few_block(const Dims& d, int rows) {
 }
 cudaError_t launch_chunk_few(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s);
 // Up to this many query rows of a kv head the tokens take the MMA's rows (chunk_narrow.cu); with 64
-// rows the narrow kernel's softmax took 1.40 ms where the wide one takes 0.89 (32 sequences of 32k).
+// rows the narrow kernel's softmax took 1.40 ms where the wide one takes 0.85 (32 sequences of 32k).
 constexpr int kNarrowRows = 32;
 cudaError_t launch_chunk_narrow(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s);
 cudaError_t launch_chunk_mma(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s);
