@@ -254,10 +254,11 @@ int kvq_free_pages(const kvq_cache* cache);
  * j % 32 of word j / 32 of its row set, in any pattern (those behind counts[b] never).  A
  * sequence may be empty; a row that sees nothing at all gives zeros.  Scores, side codes and
  * rotation as for kvq_decode_attention, the new tokens counting as fp16 tokens.
- * The tensor-core paths round each decoded key and value and each softmax weight to fp16 once, or
- * (few query rows) the products q_c * scale_c of query and key scale, which like those of the
- * decode must stay within fp16, and of weight and value scale; sums, maxima and accumulators are
- * fp32.
+ * The tensor-core paths round each decoded key and value, which must stay within fp16, and each
+ * softmax weight to fp16 once, or (up to 24 query rows of a kv head, any number with a side code)
+ * the products q_c * scale_c of query and key scale, which like those of the decode must stay
+ * within fp16, and of weight and value scale; up to four rows of a kv head those keep two fp16
+ * halves, as in the decode.  Sums, maxima and accumulators are fp32.
  * workspace: device scratch of kvq_chunk_workspace_size bytes (0: may be NULL), for the cache's
  * current lengths and kernel selection, T and num_splits (0 = automatic, else splits of the tokens of each row,
  * clamped).  status: device u32 the kernel ORs KVQ_STATUS_* bits into, never cleared here; the

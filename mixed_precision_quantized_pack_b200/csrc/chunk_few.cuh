@@ -12,8 +12,9 @@
 // movmatrix, value codes as centred subnormals (code - 2^(bits-1): their fp32 accumulators stay near
 // zero in a long context).
 //
-// Where the decode kernel splits query and weights into two fp16 halves (eight columns, four rows),
-// this one rounds them to fp16 once: twice the rows for the same work.  Sums, maxima and
+// Up to four rows, query products and weights take two columns each, their two fp16 halves, as in the
+// decode kernel (error 2e-4 against 64 bits, the output's own rounding).  From five rows on they are
+// rounded to fp16 once (10e-4): twice the rows for the same work.  Sums, maxima and
 // accumulators are fp32.  Bound: instruction issue (a code unpack per 8 to 24 rows), with the
 // cache's bytes not far below; the tcgen05 kernels decode to shared memory first, which few rows do
 // not pay for (over 32 x 32k, 16 rows 0.42 ms here and 0.59 there, 24 rows 0.56 and 0.71; K2V2 over
@@ -53,8 +54,9 @@ struct Smem {
   static_assert(kQt - kBars <= 256 && kStages % 128 == 0, "header");
 };
 
-template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int NT>
+template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int ROWS>
 struct Rings {
+  static constexpr int NT = (ROWS + 7) / 8;
   // four CTAs an SM with one n-tile, two with two or three: their accumulators spill at 168 registers
   static constexpr int CTAS = NT == 1 ? 4 : 2;
   static constexpr int AVAIL = 233472 / CTAS - 1024;
@@ -63,36 +65,50 @@ struct Rings {
   static constexpr int STAGE_F = mma::raw_stage_bytes<DK>();
   static constexpr int RING_Q = mma::ring_for(AVAIL - HDR, STAGE_Q, mma::kMinRing);
   static constexpr int RING_F = mma::ring_for(AVAIL - HDR, STAGE_F, kWarps);
-  static constexpr int MERGE = kWarps * 8 * NT * (kDV + 2) * 4;
+  static constexpr int MERGE = kWarps * ROWS * (kDV + 2) * 4;
   static constexpr int STAGES = RING_Q * STAGE_Q > RING_F * STAGE_F ? RING_Q * STAGE_Q : RING_F * STAGE_F;
   static constexpr int BYTES = HDR + (STAGES > MERGE ? STAGES : MERGE);
 };
 
-template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int NT>
-__global__ void __launch_bounds__(kThreads, Rings<KB, VB, DK, GV, GK, SR, SQ, NT>::CTAS)
+// Two weights as the fp16 pair of a B register: those of two rows, or one's halves.
+template <bool HALVES>
+__device__ __forceinline__ uint32_t weights(float w0, float w1) {
+  if constexpr (HALVES) {
+    const float hi = __half2float(__float2half_rn(w0));
+    return ptx::h2_as_u32(__floats2half2_rn(hi, w0 - hi));
+  }
+  return ptx::h2_as_u32(__floats2half2_rn(w0, w1));
+}
+
+template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int ROWS>
+__global__ void __launch_bounds__(kThreads, Rings<KB, VB, DK, GV, GK, SR, SQ, ROWS>::CTAS)
 chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBufs cb,
                  const __grid_constant__ ChunkArgs a) {
   using G = mma::Quant<KB, VB, DK, GV>;
   using R = mma::Raw<DK>;
   constexpr int KSTEPS = DK / 16;
-  using RG = Rings<KB, VB, DK, GV, GK, SR, SQ, NT>;
+  using RG = Rings<KB, VB, DK, GV, GK, SR, SQ, ROWS>;
+  constexpr int NT = RG::NT;
+  constexpr bool HALVES = ROWS == 4;         // columns 2r, 2r + 1: the two fp16 halves of row r
+  constexpr int RPT = HALVES ? 1 : 2;        // a thread's query rows per n-tile
   using SM = Smem<KSTEPS, NT, SR>;
   using Z = mma::Side<SR, SQ>;
   extern __shared__ __align__(128) unsigned char smem[];
 
-  const int split = blockIdx.x % a.splits, rb = blockIdx.x / a.splits * (8 * NT);   // the block's first query row
+  const int split = blockIdx.x % a.splits, rb = blockIdx.x / a.splits * ROWS;   // the block's first query row
   const int h = blockIdx.y, b = blockIdx.z;
   const int bh = b * d.Hkv + h;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qi = lane & 3;          // C columns 2qi, 2qi+1
   const int qr = lane >> 2;         // A rows qr, qr+8; B column qr
+  const bool low = HALVES && (qr & 1) != 0;      // the B column holds low halves
   const SeqNew sw = seq_new(a.seq, b, d.log_retain);
   if (sw.n == 0) return;
   const int n_rows = d.n_rep * a.T;
   // the new tokens that some row of the block may see; none of its rows may be valid
   int n_vis = sw.n;
   {
-    const int r1 = min(rb + 8 * NT, n_rows) - 1;
+    const int r1 = min(rb + ROWS, n_rows) - 1;
     if (rb / a.T == r1 / a.T) {                 // rows of one head: tokens rb % T to r1 % T
       if (rb % a.T >= sw.n) return;
       if (!a.mask) n_vis = min(n_vis, r1 % a.T + 1);
@@ -125,7 +141,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   bool qok[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = rb + 8 * nt + qr;
+    const int r = rb + 8 * nt + (HALVES ? qr >> 1 : qr);
     qok[nt] = r < n_rows && r % a.T < sw.n;
     qrow[nt] = a.q + (static_cast<size_t>(bh) * n_rows + (qok[nt] ? r : 0)) * DK;
   }
@@ -146,14 +162,14 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   }
   const int n_units = unit_end - unit_begin;
 
-  // softmax state of rows 8nt + 2qi and 8nt + 2qi + 1 over this warp's tokens
-  float m_run[NT][2], l_run[NT][2];
-  float zsum[G::NVG][NT][2];               // sum_j p_j z_{j,g}, lane-partial
+  // softmax state of rows 8nt + 2qi and 8nt + 2qi + 1 (HALVES: row qi) over this warp's tokens
+  float m_run[NT][RPT], l_run[NT][RPT];
+  float zsum[G::NVG][NT][RPT];             // sum_j p_j z_{j,g}, lane-partial
   float co[NT][8][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < RPT; ++i) {
       m_run[nt][i] = -INFINITY;
       l_run[nt][i] = 0.0f;
 #pragma unroll
@@ -174,24 +190,23 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   // in [2^11, 2^15], whatever the values' magnitude (unlifted, values around 1e-4 came out with errors
   // of a percent: their products with most weights are subnormal).  A scale above 2^(15 - lift) moves
   // it; the smallest one there is, 2^-24, passes the initial 2^-49.  The fp16 list keeps 0: its weights
-  // are rounded without a scale.  The check costs up to 3% (units of 32 tokens; with a side code and
-  // three n-tiles 6%).
+  // are rounded without a scale.  The check costs 0 to 3%.
   float lift = quant ? 64.0f : 0.0f;
 
   auto scale_row = [&](int nt, float f0, float f1) {
     l_run[nt][0] *= f0;
-    l_run[nt][1] *= f1;
+    if constexpr (!HALVES) l_run[nt][RPT - 1] *= f1;
 #pragma unroll
     for (int g = 0; g < G::NVG; ++g) {
       zsum[g][nt][0] *= f0;
-      zsum[g][nt][1] *= f1;
+      if constexpr (!HALVES) zsum[g][nt][RPT - 1] *= f1;
     }
 #pragma unroll
     for (int mv = 0; mv < 8; ++mv) {
       co[nt][mv][0] *= f0;
-      co[nt][mv][1] *= f1;
+      co[nt][mv][1] *= HALVES ? f0 : f1;
       co[nt][mv][2] *= f0;
-      co[nt][mv][3] *= f1;
+      co[nt][mv][3] *= HALVES ? f0 : f1;
     }
   };
   // Moves the references of an n-tile's rows to their maxima.  They do not lag behind: weights stay at
@@ -200,13 +215,13 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       g0 = fmaxf(g0, __shfl_xor_sync(0xffffffffu, g0, o));
-      g1 = fmaxf(g1, __shfl_xor_sync(0xffffffffu, g1, o));
+      if constexpr (!HALVES) g1 = fmaxf(g1, __shfl_xor_sync(0xffffffffu, g1, o));
     }
-    const bool mv0 = g0 > m_run[nt][0], mv1 = g1 > m_run[nt][1];
+    const bool mv0 = g0 > m_run[nt][0], mv1 = !HALVES && g1 > m_run[nt][RPT - 1];
     if (__any_sync(0xffffffffu, mv0 || mv1)) {
-      const float f0 = mv0 ? ptx::ex2(m_run[nt][0] - g0) : 1.0f, f1 = mv1 ? ptx::ex2(m_run[nt][1] - g1) : 1.0f;
+      const float f0 = mv0 ? ptx::ex2(m_run[nt][0] - g0) : 1.0f, f1 = mv1 ? ptx::ex2(m_run[nt][RPT - 1] - g1) : 1.0f;
       if (mv0) m_run[nt][0] = g0;
-      if (mv1) m_run[nt][1] = g1;
+      if (mv1) m_run[nt][RPT - 1] = g1;
       scale_row(nt, f0, f1);
     }
   };
@@ -325,6 +340,25 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
       const uint32_t* svc = reinterpret_cast<const uint32_t*>(S + L.v_off);
       const uint32_t* svm = reinterpret_cast<const uint32_t*>(S + L.vmeta_off);
 
+      // ---- the lift of the weights follows the group's value scales ----
+      {
+        constexpr int W = GK * G::NVG / 32;      // the lane's share of the (scale, zero) pairs
+        uint32_t sz[W];
+        mma::load_words<W>(svm + lane * W, sz);
+        __half2 mx = ptx::u32_as_h2(sz[0]);
+#pragma unroll
+        for (int i = 1; i < W; ++i) mx = __hmax2(mx, ptx::u32_as_h2(sz[i]));
+        float top = __low2float(mx);
+        if (__any_sync(0xffffffffu, top > ptx::ex2(15.0f - lift))) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;      // 2^e <= top < 2^(e + 1)
+          const float to = static_cast<float>(11 - e), f = ptx::ex2(to - lift);
+          lift = to;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) scale_row(nt, f, f);
+        }
+      }
       // ---- group prologue: B = q * s, and the zero-point bias ----
       uint32_t bq[NT][KSTEPS][2];
       float cbias[NT][4];
@@ -363,7 +397,8 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
               // the word's block holds (s_c, s_c+16/KB) for each register, then the zeros
               const int rho = 2 * ls + j;
               za[j] = meta[G::RPW + rho];
-              bq[nt][s][j] = ptx::h2_as_u32(__hmul2(ptx::u32_as_h2(qfx[2 * ls + j]), ptx::u32_as_h2(meta[rho])));
+              const __half2 qs = ptx::u32_as_h2(qfx[2 * ls + j]), sc = ptx::u32_as_h2(meta[rho]), hi = __hmul2(qs, sc);
+              bq[nt][s][j] = ptx::h2_as_u32(low ? __hfma2(qs, sc, __hneg2(hi)) : hi);
             }
             ptx::mma_16816(cbias[nt], za[0], za[0], za[1], za[1], qbx[2 * ls], qbx[2 * ls + 1]);
           }
@@ -379,21 +414,23 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
           bz[nt] = 0u;
           if (qi < Z::NQ) {
             const float f = 1.0f / static_cast<float>(1 << Z::pos(qi));
-            const float* qt = sm_qt + (8 * nt + qr) * SR;
-            bz[nt] = ptx::h2_as_u32(__floats2half2_rn(qt[qi] * __low2float(zm[qi]) * f,
-                                                      qt[qi + Z::NQ] * __low2float(zm[qi + Z::NQ]) * f));
+            const float* qt = sm_qt + (8 * nt + (HALVES ? qr >> 1 : qr)) * SR;
+            const float x0 = qt[qi] * __low2float(zm[qi]) * f, x1 = qt[qi + Z::NQ] * __low2float(zm[qi + Z::NQ]) * f;
+            const __half2 hi = __floats2half2_rn(x0, x1);
+            bz[nt] = ptx::h2_as_u32(low ? __floats2half2_rn(x0 - __low2float(hi), x1 - __high2float(hi)) : hi);
           }
 #pragma unroll
           for (int i = 0; i < SR; ++i) {
             const float zero = __high2float(zm[i]);
-            cbias[nt][0] = fmaf(sm_qt[(8 * nt + 2 * qi) * SR + i], zero, cbias[nt][0]);
-            cbias[nt][1] = fmaf(sm_qt[(8 * nt + 2 * qi + 1) * SR + i], zero, cbias[nt][1]);
+#pragma unroll
+            for (int r = 0; r < RPT; ++r)
+              cbias[nt][r] = fmaf(sm_qt[(8 * nt + RPT * qi + r) * SR + i], zero, cbias[nt][r]);
           }
         }
       }
 
-      // ---- scores of the whole group: tokens 16 mt + qr, + 8; rows 2qi, 2qi + 1 of every n-tile ----
-      float sc[NT][MT][4];
+      // ---- scores of the whole group: tokens 16 mt + qr, + 8; the thread's rows of every n-tile ----
+      float sc[NT][MT][2 * RPT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float cs[NT][4];
@@ -436,7 +473,8 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[nt][mt][e] = fmaf(cs[nt][e], alpha24, cbias[nt][e & 1] * alpha);
+          for (int e = 0; e < 2 * RPT; ++e)
+            sc[nt][mt][e] = fmaf(HALVES ? cs[nt][2 * e] + cs[nt][2 * e + 1] : cs[nt][e], alpha24, cbias[nt][e % RPT] * alpha);
       }
       // retained tokens of this group are read from the fp16 list: mask them here
       const int g0 = (unit_begin + k) * GK;
@@ -449,55 +487,37 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (off == 16 * mt + qr) sc[nt][mt][0] = sc[nt][mt][1] = -INFINITY;
-            if (off == 16 * mt + qr + 8) sc[nt][mt][2] = sc[nt][mt][3] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 2 * RPT; ++e)
+              if (off == 16 * mt + qr + (e / RPT) * 8) sc[nt][mt][e] = -INFINITY;
           }
       }
-      // ---- the lift of the weights follows the group's value scales ----
-      {
-        constexpr int W = GK * G::NVG / 32;      // the lane's share of the (scale, zero) pairs
-        uint32_t sz[W];
-        mma::load_words<W>(svm + lane * W, sz);
-        __half2 mx = ptx::u32_as_h2(sz[0]);
-#pragma unroll
-        for (int i = 1; i < W; ++i) mx = __hmax2(mx, ptx::u32_as_h2(sz[i]));
-        float top = __low2float(mx);
-        if (__any_sync(0xffffffffu, top > ptx::ex2(15.0f - lift))) {
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;      // 2^e <= top < 2^(e + 1)
-          const float to = static_cast<float>(11 - e), f = ptx::ex2(to - lift);
-          lift = to;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) scale_row(nt, f, f);
-        }
-      }
       // ---- online softmax update for the group ----
-      float m_use[NT][2];
+      float m_use[NT][RPT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          x0 = fmaxf(x0, fmaxf(sc[nt][mt][0], sc[nt][mt][2]));
-          x1 = fmaxf(x1, fmaxf(sc[nt][mt][1], sc[nt][mt][3]));
+          x0 = fmaxf(x0, fmaxf(sc[nt][mt][0], sc[nt][mt][RPT]));
+          x1 = fmaxf(x1, fmaxf(sc[nt][mt][RPT - 1], sc[nt][mt][2 * RPT - 1]));
         }
         rescale(nt, x0, x1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) m_use[nt][i] = (m_run[nt][i] == -INFINITY ? 0.0f : m_run[nt][i]) - lift;
+        for (int i = 0; i < RPT; ++i) m_use[nt][i] = (m_run[nt][i] == -INFINITY ? 0.0f : m_run[nt][i]) - lift;
       }
 
       // ---- p.V over the group ----
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const int t0 = 16 * mt + qr;
-        float p[NT][4];
+        float p[NT][2 * RPT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[nt][e] = ptx::ex2(sc[nt][mt][e] - m_use[nt][e & 1]);
-          l_run[nt][0] += p[nt][0] + p[nt][2];
-          l_run[nt][1] += p[nt][1] + p[nt][3];
+          for (int e = 0; e < 2 * RPT; ++e) p[nt][e] = ptx::ex2(sc[nt][mt][e] - m_use[nt][e % RPT]);
+#pragma unroll
+          for (int i = 0; i < RPT; ++i) l_run[nt][i] += p[nt][i] + p[nt][RPT + i];
         }
         // value (scale, zero) of the two tokens this thread weights
         uint32_t vm0[G::NVG], vm1[G::NVG];
@@ -525,10 +545,11 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
           uint32_t bp[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            zsum[gg][nt][0] = fmaf(p[nt][0], zc0, fmaf(p[nt][2], zc1, zsum[gg][nt][0]));
-            zsum[gg][nt][1] = fmaf(p[nt][1], zc0, fmaf(p[nt][3], zc1, zsum[gg][nt][1]));
-            bp[nt][0] = ptx::movmatrix_trans(ptx::h2_as_u32(__floats2half2_rn(p[nt][0] * f0.x, p[nt][1] * f0.x)));
-            bp[nt][1] = ptx::movmatrix_trans(ptx::h2_as_u32(__floats2half2_rn(p[nt][2] * f1.x, p[nt][3] * f1.x)));
+#pragma unroll
+            for (int i = 0; i < RPT; ++i)
+              zsum[gg][nt][i] = fmaf(p[nt][i], zc0, fmaf(p[nt][RPT + i], zc1, zsum[gg][nt][i]));
+            bp[nt][0] = ptx::movmatrix_trans(weights<HALVES>(p[nt][0] * f0.x, p[nt][RPT - 1] * f0.x));
+            bp[nt][1] = ptx::movmatrix_trans(weights<HALVES>(p[nt][RPT] * f1.x, p[nt][2 * RPT - 1] * f1.x));
           }
           const int bit0 = (gg * GV + qr * G::CPG) * VB;
           const int wv = bit0 >> 5, ob = bit0 & 31;
@@ -589,7 +610,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int c = 16 * s + 2 * qi + 8 * j;
-          qn[nt][s][j] = qok[nt] ? ptx::h2_as_u32(__halves2half2(qrow[nt][c], qrow[nt][c + 1])) : 0u;
+          qn[nt][s][j] = qok[nt] && !low ? ptx::h2_as_u32(__halves2half2(qrow[nt][c], qrow[nt][c + 1])) : 0u;
         }
     // stale shared memory must hold finite values: masked rows multiply p = 0
     for (int i = threadIdx.x; i < RING * STAGE / 16; i += kThreads)
@@ -672,19 +693,22 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          cs[nt][e] = sees(e0 + qr + 8 * (e >> 1), rb + 8 * nt + 2 * qi + (e & 1)) ? cs[nt][e] * alpha : -INFINITY;
-        rescale(nt, fmaxf(cs[nt][0], cs[nt][2]), fmaxf(cs[nt][1], cs[nt][3]));
-        float p[4];
+        for (int e = 0; e < 2 * RPT; ++e) {
+          // (HALVES: the queries stand in the high columns alone)
+          const float x = cs[nt][HALVES ? 2 * e : e];
+          cs[nt][e] = sees(e0 + qr + 8 * (e / RPT), rb + 8 * nt + RPT * qi + e % RPT) ? x * alpha : -INFINITY;
+        }
+        rescale(nt, fmaxf(cs[nt][0], cs[nt][RPT]), fmaxf(cs[nt][RPT - 1], cs[nt][2 * RPT - 1]));
+        float p[2 * RPT];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float m = m_run[nt][e & 1];
+        for (int e = 0; e < 2 * RPT; ++e) {
+          const float m = m_run[nt][e % RPT];
           p[e] = ptx::ex2(cs[nt][e] - (m == -INFINITY ? 0.0f : m));
         }
-        l_run[nt][0] += p[0] + p[2];
-        l_run[nt][1] += p[1] + p[3];
-        bp[nt][0] = ptx::movmatrix_trans(ptx::h2_as_u32(__floats2half2_rn(p[0], p[1])));
-        bp[nt][1] = ptx::movmatrix_trans(ptx::h2_as_u32(__floats2half2_rn(p[2], p[3])));
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) l_run[nt][i] += p[i] + p[RPT + i];
+        bp[nt][0] = ptx::movmatrix_trans(weights<HALVES>(p[0], p[RPT - 1]));
+        bp[nt][1] = ptx::movmatrix_trans(weights<HALVES>(p[RPT], p[2 * RPT - 1]));
       }
       // p.V: A = V^T tiles via ldmatrix.trans (rows = tokens in shared memory)
       const int vrow = (mi >> 1) * 8 + (lane & 7);
@@ -721,7 +745,7 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < RPT; ++i) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         l_run[nt][i] += __shfl_xor_sync(0xffffffffu, l_run[nt][i], o);
@@ -734,18 +758,22 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
       }
     }
   __syncthreads();   // every warp is done with the stages: reuse them for the merge
-  constexpr int NR = 8 * NT;
+  constexpr int NR = ROWS;
   float* sm_o = reinterpret_cast<float*>(smem + SM::kStages);        // [kWarps][NR][kDV]
   float* sm_ml = sm_o + kWarps * NR * kDV;                           // [kWarps][NR][2]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 8 * nt + 2 * qi + i;
+    for (int i = 0; i < RPT; ++i) {
+      const int r = 8 * nt + RPT * qi + i;
       float* dst = sm_o + (warp * NR + r) * kDV;
 #pragma unroll
       for (int mv = 0; mv < 8; ++mv) {
         float o0 = co[nt][mv][i], o1 = co[nt][mv][2 + i];
+        if constexpr (HALVES) {
+          o0 += co[nt][mv][1];
+          o1 += co[nt][mv][3];
+        }
         int c0, c1;
         if (quant) {
           const int gg = mv / G::MPG, ml = mv % G::MPG;
@@ -791,14 +819,14 @@ chunk_few_kernel(const __grid_constant__ Dims d, const __grid_constant__ CacheBu
   }
 }
 
-template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int NT>
+template <int KB, int VB, int DK, int GV, int GK, int SR, int SQ, int ROWS>
 cudaError_t launch(const Dims& d, const CacheBufs& c, const ChunkArgs& a, cudaStream_t s) {
-  using RG = Rings<KB, VB, DK, GV, GK, SR, SQ, NT>;
+  using RG = Rings<KB, VB, DK, GV, GK, SR, SQ, ROWS>;
   static SmemLimit limit;
-  const cudaError_t e = limit.raise(chunk_few_kernel<KB, VB, DK, GV, GK, SR, SQ, NT>, RG::BYTES);
+  const cudaError_t e = limit.raise(chunk_few_kernel<KB, VB, DK, GV, GK, SR, SQ, ROWS>, RG::BYTES);
   if (e != cudaSuccess) return e;
-  const int blocks = (d.n_rep * a.T + 8 * NT - 1) / (8 * NT);
-  chunk_few_kernel<KB, VB, DK, GV, GK, SR, SQ, NT><<<dim3(a.splits * blocks, d.Hkv, d.B), kThreads, RG::BYTES, s>>>(d, c, a);
+  const int blocks = (d.n_rep * a.T + ROWS - 1) / ROWS;
+  chunk_few_kernel<KB, VB, DK, GV, GK, SR, SQ, ROWS><<<dim3(a.splits * blocks, d.Hkv, d.B), kThreads, RG::BYTES, s>>>(d, c, a);
   return cudaGetLastError();
 }
 
@@ -823,9 +851,10 @@ LaunchFn find_side(const Dims& d, int rows);
 #define KVQ_CHUNK_FEW_ENTRY(KB, VB, DK, GV, GK, SR, SQ)                                        \
   if (d.kb == KB && d.vb == VB && d.dk == DK && d.gv == GV && d.gk == GK && d.sr == SR &&      \
       (SR == 0 || d.sq == SQ))                                                                 \
-    return chunk_few_block(d, rows) == 8    ? &launch<KB, VB, DK, GV, GK, SR, SQ, 1>              \
-           : chunk_few_block(d, rows) == 16 ? &launch<KB, VB, DK, GV, GK, SR, SQ, 2>              \
-                                         : &launch<KB, VB, DK, GV, GK, SR, SQ, 3>;
+    return chunk_few_block(d, rows) == 4    ? &launch<KB, VB, DK, GV, GK, SR, SQ, 4>              \
+           : chunk_few_block(d, rows) == 8  ? &launch<KB, VB, DK, GV, GK, SR, SQ, 8>              \
+           : chunk_few_block(d, rows) == 16 ? &launch<KB, VB, DK, GV, GK, SR, SQ, 16>             \
+                                            : &launch<KB, VB, DK, GV, GK, SR, SQ, 24>;
 
 }  // namespace few
 }  // namespace kvq

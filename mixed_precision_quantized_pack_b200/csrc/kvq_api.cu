@@ -1107,7 +1107,7 @@ struct ChunkPlan {
 int few_splits(const kvq::Dims& d, int nG, double mean, int nF, int rows, int sm_count) {
   const int block = kvq::chunk_few_block(d, rows);
   const double units = static_cast<double>(d.B) * d.Hkv * ((rows + block - 1) / block);
-  const double sms = sm_count, fixed = block == 8 ? 512.0 : 256.0, list = nF + fixed;
+  const double sms = sm_count, fixed = block <= 8 ? 512.0 : 256.0, list = nF + fixed;
   const int hi = std::min(nG, split_cap(d));
   int best = 1;
   double best_t = 0.0;
@@ -1118,7 +1118,7 @@ int few_splits(const kvq::Dims& d, int nG, double mean, int nF, int rows, int sm
     double t;
     if (all <= sms)
       t = most;
-    else if (block == 8)
+    else if (block <= 8)
       t = most + (ceil(all / sms) - 1.0) * cta;
     else if (all <= 2 * sms)
       t = most + cta;
@@ -1181,7 +1181,7 @@ int plan_chunk(const kvq_cache* c, int T, int num_splits, ChunkPlan* p) {
     const int block = kvq::chunk_few_block(d, d.n_rep * T);
     const long long blocks = (static_cast<long long>(d.n_rep) * T + block - 1) / block;
     if (blocks > 1 && (num_splits == 0 || nG > 0)) {
-      const long long ctas = (block == 8 ? 4LL : 2LL) * c->sm_count / (blocks * d.B * d.Hkv) - p->splits_q;
+      const long long ctas = (block <= 8 ? 4LL : 2LL) * c->sm_count / (blocks * d.B * d.Hkv) - p->splits_q;
       list = static_cast<int>(std::max(1LL, std::min<long long>(list, ctas)));
     }
     p->splits = p->splits_q + list;

@@ -137,3 +137,29 @@ def test_chunk_padding_is_not_worked_through(extra):
     assert count(40, [18, 0, 2]) <= count(18, [18, 0, 2]) + 1
     check_chunk(tw, 40, counts=[18, 0, 2], kernels=(K.KVQ_KERNEL_TENSOR,))
     check_chunk(tw, 40, counts=[3, 1, 2], kernels=(K.KVQ_KERNEL_TENSOR,))
+
+
+@pytest.mark.parametrize("extra", [dict(), dict(k_bits=2), dict(v_bits=4), dict(k_bits=8, v_bits=4), dict(d_k=32),
+                                   dict(group_k=32, group_v=32), dict(side_rank=4, side_bits=4),
+                                   dict(side_rank=8, side_bits=4, rot_keys=1), dict(paged=1, n_q_heads=2)])
+def test_chunk_of_up_to_four_rows_is_as_exact_as_a_decode(extra):
+    """Up to four query rows of a kv head nothing but the output is rounded to 11 bits.
+
+    The output's rounding is off by at most 2^-11 of an element and spread evenly over that, so its
+    2-norm is at most 2^-11 / sqrt(3) = 2.8e-4 of the output's; halves of 11 bits each leave 2^-22 of
+    a product, and MMAs that truncate fp32 sums at most 2^-22 a step over 4000 / 16 steps: 6e-5."""
+    n_rep = extra.get("n_q_heads", 8) // 2
+    for lengths in ([4000, 300, 1], [129, 0, 64]):
+        tw = Twin(config(max_context=4096, **extra), lengths, seed=3)
+        for T in (1, 2, 4):
+            if n_rep * T > 4:
+                continue
+            check_chunk(tw, T, splits=(0, 1, 3), kernels=KERNELS[:1])
+            q, k_new, v_new = tw.chunk(T)
+            for ns in (0, 1):
+                got = tw.gc.chunk_attention(*[torch.from_numpy(x).cuda() for x in (q, k_new, v_new)], num_splits=ns)
+                got = got.double().cpu().numpy()
+                for b in range(3):
+                    ref, _ = seq_ops.reference(tw, b, q[b], k_new[b], v_new[b], seq_ops.causal(T))
+                    err = np.linalg.norm(got[b] - ref) / np.linalg.norm(ref)
+                    assert err <= 3.4e-4, (lengths, T, ns, b, err)
