@@ -17,7 +17,7 @@
 // rounded to fp16 once (10e-4): twice the rows for the same work.  Sums, maxima and
 // accumulators are fp32.  Bound: instruction issue (a code unpack per 8 to 24 rows), with the
 // cache's bytes not far below; the tcgen05 kernels decode to shared memory first, which few rows do
-// not pay for (over 32 x 32k, 16 rows 0.42 ms here and 0.59 there, 24 rows 0.56 and 0.71; K2V2 over
+// not pay for (over 32 x 32k, 16 rows 0.42 ms here and 0.59 there, 24 rows 0.57 and 0.71; K2V2 over
 // 16 x 16k, 24 rows 0.17 and 0.22; K4V4 0.18 and 0.20).  Groups of 32 with 4-bit keys and 2-bit values
 // are about even at 17 to 24 rows (20 rows, 8 kv heads: 4 x 32k 111 us here and 131 there, 12 x 2k 46
 // and 66, 8 x 16k 124 and 125; 16 x 16k 221 and 214, 12 x 8k 133 and 113, 16 x 2k 66 and 55).  A fourth

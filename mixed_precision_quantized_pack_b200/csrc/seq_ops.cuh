@@ -130,8 +130,8 @@ bool chunk_mma_supported(const Dims& d);
 bool chunk_few_supported(const Dims& d, int T);
 // Query rows that a block of the few-row kernel takes, of `rows` in all: half an n-tile of 8 columns (two
 // columns a row), or one to three of them.
-// With a side code three tiles spill 560 to 640 bytes a thread (4-bit keys), but two blocks of 16 read
-// the cache twice: 24 rows over 16 x 16k 203 us and 265, 4 x 32k 105 and 155, 16 x 1k 48 and 70 (8 kv
+// With a side code three tiles spill about 580 bytes a thread (4-bit keys), but two blocks of 16 read
+// the cache twice: 24 rows over 16 x 16k 198 us and 265, 4 x 32k 105 and 155, 16 x 1k 48 and 70 (8 kv
 // heads; in between, from 4 sequences on, either is ahead, 16 x 2k 80 and 80, 4 x 4k 48 and 41).  Up to
 // 3 sequences two blocks are: 1 x 4k 36 and 30, 1 x 32k 60 and 56, 3 x 8k 52 and 44.  Without a side
 // code the other side of the rule is the narrow kernel.
